@@ -63,6 +63,17 @@ _SIGS = {
     "moe_seq_balance_loss_workspace_size": (_i, [_i, _i, _i, _c.POINTER(_sz)]),
     "moe_seq_balance_loss": (_i, [_p, _i, _i, _i, _i, _f, _p, _p, _p, _p, _sz, _p]),
     "moe_fp8_mma_peak": (_i, [_i, _i, _i, _p, _p, _p]),
+    "moe_sort_rows": (_i, [_p, _i, _i64, _p, _i, _i, _i, _p, _i64, _i64, _p, _p]),
+    "moe_sort_rows_backward": (_i, [_p, _i, _i64, _i64, _p, _i, _i, _i, _p, _i64, _p, _p]),
+    "moe_unsort_rows": (_i, [_p, _i, _i64, _i64, _p, _p, _i, _i, _i, _p, _i64, _p, _p]),
+    "moe_unsort_rows_backward": (_i, [_p, _i, _i64, _p, _i64, _p, _p, _i, _i, _i, _p, _i64, _i64,
+                                      _p, _p, _p]),
+    "moe_combine_checkpoint": (_i, [_p, _i64, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _p]),
+    "moe_combine_checkpoint_backward": (_i, [_p, _p, _p, _p, _p, _i64, _i, _i, _i, _p, _p, _p, _p,
+                                             _p, _p]),
+    "moe_route_backward_workspace_size": (_i, [_i, _i, _i, _c.POINTER(_sz)]),
+    "moe_route_backward": (_i, [_p, _p, _p, _p, _p, _i64, _p, _i, _i, _i, _i, _p, _p, _i, _f, _p,
+                                _p, _p, _p, _p, _sz, _p, _p]),
 }
 
 EP_F32 = 0
@@ -110,7 +121,10 @@ LAUNCHES_PER_CALL = {"fp8_quant_1x128": 1, "fp8_quant_128x128": 1, "swiglu_quant
                      "moe_permute_index": 2, "fp8_quant_1x128_scatter": 1,
                      "moe_tile_table": 1, "moe_segment_ids": 1,
                      "grouped_gemm_fp8_blockscaled": 1, "moe_combine": 1, "moe_bias_update": 1,
-                     "moe_seq_balance_loss": 3, "moe_fp8_mma_peak": 1}
+                     "moe_seq_balance_loss": 3, "moe_fp8_mma_peak": 1,
+                     "moe_sort_rows": 1, "moe_sort_rows_backward": 1, "moe_unsort_rows": 1,
+                     "moe_unsort_rows_backward": 1, "moe_combine_checkpoint": 1,
+                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 3}
 launch_count = 0
 
 
@@ -627,3 +641,267 @@ def grouped_gemm_fp8_wgrad(At, a_atoms, Bt, b_atoms, tile_start, groups, dW=None
                                         Nb, _ptr(tile_start), groups, _ptr(dW), _ptr(dev_err),
                                         _stream(stream)), "grouped_gemm_fp8_wgrad")
     return dW
+
+
+# --------------------------------------- tokens sorted by expert and back ---
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise MoEError(what)
+
+
+def _here(what: str, *tensors) -> torch.device:
+    """The device of the tensors (None skipped): one device for all of them,
+    and the current one, whose stream the call is queued on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        _need(t.is_cuda, f"{what}: expected a CUDA tensor")
+        dev = t.device if dev is None else dev
+        _need(t.device == dev, f"{what}: tensors on different devices")
+    _need(dev.index == torch.cuda.current_device(),
+          f"{what}: the tensors are not on the current device")
+    return dev
+
+
+def _rows2d(what: str, name: str, t, d=None, n=None, dtype=None):
+    """Checks a matrix of contiguous rows (any row stride >= d)."""
+    _need(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1),
+          f"{what}: {name} must be a matrix with contiguous rows")
+    _need(d is None or t.shape[1] == d, f"{what}: {name} has {t.shape[1]} columns, expected {d}")
+    _need(n is None or t.shape[0] == n, f"{what}: {name} has {t.shape[0]} rows, expected {n}")
+    _need(dtype is None or t.dtype == dtype, f"{what}: {name} must be {dtype}")
+    # the row stride of a single row says nothing
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _dense(what: str, name: str, t, dtype, shape):
+    _need(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          f"{what}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _table(what: str, dst_of):
+    _need(dst_of.dim() == 2 and dst_of.dtype == torch.int32 and dst_of.is_contiguous(),
+          f"{what}: dst_of must be a contiguous int32 [T][K] table")
+    return dst_of.shape
+
+
+def _row_type(what: str, t) -> int:
+    _need(t.dtype in _DTYPES, f"{what}: rows must be bf16, fp16 or fp32")
+    return _DTYPES[t.dtype]
+
+
+def moe_sort_rows(x, dst_of, rows=None, out=None, dev_err=None, stream=None):
+    """x [T][d] (bf16, fp16 or fp32; row stride may exceed d) -> xs [rows][d]
+    with xs[dst_of[t][k]] = x[t]; rows defaults to T*K.  Rows of a given
+    ``out`` that no pair points at stay as they were (undefined in a new one)."""
+    what = "moe_sort_rows"
+    T, K = _table(what, dst_of)
+    dt = _row_type(what, x)
+    ldx = _rows2d(what, "x", x, n=T)
+    d = x.shape[1]
+    dev = _here(what, x, dst_of, out, dev_err)
+    if out is None:
+        out = torch.empty(T * K if rows is None else rows, d, dtype=x.dtype, device=dev)
+    ldo = _rows2d(what, "out", out, d, rows, x.dtype)
+    _count(what)
+    _check(lib().moe_sort_rows(x.data_ptr(), dt, ldx, dst_of.data_ptr(), T, K, d, out.data_ptr(),
+                               ldo, out.shape[0], _ptr(dev_err), _stream(stream)), what)
+    return out
+
+
+def moe_sort_rows_backward(dxs, dst_of, dx=None, dev_err=None, stream=None):
+    """dxs [rows][d] -> dx [T][d] with dx[t] = sum_k dxs[dst_of[t][k]]."""
+    what = "moe_sort_rows_backward"
+    T, K = _table(what, dst_of)
+    dt = _row_type(what, dxs)
+    lds = _rows2d(what, "dxs", dxs)
+    n, d = dxs.shape
+    dev = _here(what, dxs, dst_of, dx, dev_err)
+    if dx is None:
+        dx = torch.empty(T, d, dtype=dxs.dtype, device=dev)
+    ldx = _rows2d(what, "dx", dx, d, T, dxs.dtype)
+    _count(what)
+    _check(lib().moe_sort_rows_backward(dxs.data_ptr(), dt, lds, n, dst_of.data_ptr(), T, K, d,
+                                        dx.data_ptr(), ldx, _ptr(dev_err), _stream(stream)), what)
+    return dx
+
+
+def moe_unsort_rows(y, dst_of, weight, out=None, dev_err=None, stream=None):
+    """y [rows][d], weight fp32 [T][K] -> out [T][d] with
+    out[t] = sum_k weight[t][k] y[dst_of[t][k]]."""
+    what = "moe_unsort_rows"
+    T, K = _table(what, dst_of)
+    dt = _row_type(what, y)
+    ldy = _rows2d(what, "y", y)
+    _dense(what, "weight", weight, torch.float32, (T, K))
+    n, d = y.shape
+    dev = _here(what, y, dst_of, weight, out, dev_err)
+    if out is None:
+        out = torch.empty(T, d, dtype=y.dtype, device=dev)
+    ldo = _rows2d(what, "out", out, d, T, y.dtype)
+    _count(what)
+    _check(lib().moe_unsort_rows(y.data_ptr(), dt, ldy, n, dst_of.data_ptr(), weight.data_ptr(), T,
+                                 K, d, out.data_ptr(), ldo, _ptr(dev_err), _stream(stream)), what)
+    return out
+
+
+def moe_unsort_rows_backward(dout, y, dst_of, weight, dy=None, dweight=None, want_dy=True,
+                             want_dweight=True, dev_err=None, stream=None):
+    """dout [T][d], y [rows][d] -> (dy [rows][d], dweight fp32 [T][K]) with
+    dy[dst_of[t][k]] = weight[t][k] dout[t] and dweight[t][k] = dout[t] .
+    y[dst_of[t][k]]; either is None where it is not wanted.  Rows of a given
+    ``dy`` that no pair points at stay as they were (undefined in a new one)."""
+    what = "moe_unsort_rows_backward"
+    T, K = _table(what, dst_of)
+    dt = _row_type(what, dout)
+    ldo = _rows2d(what, "dout", dout, n=T)
+    d = dout.shape[1]
+    ldy = _rows2d(what, "y", y, d, dtype=dout.dtype)
+    _dense(what, "weight", weight, torch.float32, (T, K))
+    n = y.shape[0]
+    dev = _here(what, dout, y, dst_of, weight, dy, dweight, dev_err)
+    want_dy, want_dweight = want_dy or dy is not None, want_dweight or dweight is not None
+    _need(want_dy or want_dweight, f"{what}: neither gradient wanted")
+    lddy = 0
+    if want_dy:
+        if dy is None:
+            dy = torch.empty(n, d, dtype=dout.dtype, device=dev)
+        lddy = _rows2d(what, "dy", dy, d, n, dout.dtype)
+    if want_dweight:
+        if dweight is None:
+            dweight = torch.empty(T, K, dtype=torch.float32, device=dev)
+        _dense(what, "dweight", dweight, torch.float32, (T, K))
+    _count(what)
+    _check(lib().moe_unsort_rows_backward(dout.data_ptr(), dt, ldo, y.data_ptr(), ldy,
+                                          dst_of.data_ptr(), weight.data_ptr(), T, K, d, _ptr(dy),
+                                          lddy, n, _ptr(dweight), _ptr(dev_err), _stream(stream)),
+           what)
+    return dy, dweight
+
+
+# ------------------------------------------- 8-bit checkpoint of the combine ---
+def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None, ys=None,
+                           pow2=False, dev_err=None, stream=None):
+    """moe_combine that also keeps Y in 8 bits: Y fp32 [rows][d] ->
+    (out fp32 [T][d], yq uint8 [rows][d], ys fp32 [rows][d/128]).  Rows that
+    no pair points at stay as they were (undefined in new buffers)."""
+    what = "moe_combine_checkpoint"
+    T, K = _table(what, dst_of)
+    _need(Y.dim() == 2, f"{what}: Y must be a matrix")
+    rows, d = Y.shape
+    _need(d % 128 == 0, f"{what}: d must be a multiple of 128")
+    _dense(what, "Y", Y, torch.float32, (rows, d))
+    _dense(what, "topk_gate", topk_gate, torch.float32, (T, K))
+    _dense(what, "u", u, torch.bfloat16, (T, d))
+    if Y_shared is not None:
+        _dense(what, "Y_shared", Y_shared, torch.float32, (T, d))
+    dev = _here(what, Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, dev_err)
+    out = torch.empty(T, d, dtype=torch.float32, device=dev) if out is None else out
+    yq = torch.empty(rows, d, dtype=torch.uint8, device=dev) if yq is None else yq
+    ys = torch.empty(rows, d // 128, dtype=torch.float32, device=dev) if ys is None else ys
+    _dense(what, "out", out, torch.float32, (T, d))
+    _dense(what, "yq", yq, torch.uint8, (rows, d))
+    _dense(what, "ys", ys, torch.float32, (rows, d // 128))
+    _count(what)
+    _check(lib().moe_combine_checkpoint(Y.data_ptr(), rows, dst_of.data_ptr(), topk_gate.data_ptr(),
+                                        _ptr(Y_shared), u.data_ptr(), T, K, d, int(bool(pow2)),
+                                        out.data_ptr(), yq.data_ptr(), ys.data_ptr(), _ptr(dev_err),
+                                        _stream(stream)), what)
+    return out, yq, ys
+
+
+def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, dys=None, dy=None,
+                                    dgate=None, want_dy=False, dev_err=None, stream=None):
+    """dout fp32 [T][d] and the checkpoint (yq, ys) -> (dyq uint8 [T*K+T][d],
+    dys [T*K+T][d/128], dy fp32 or None, dgate fp32 [T][K])."""
+    what = "moe_combine_checkpoint_backward"
+    T, K = _table(what, dst_of)
+    _need(dout.dim() == 2 and dout.shape[0] == T and dout.shape[1] % 128 == 0,
+          f"{what}: dout must be [T][d] with d a multiple of 128")
+    d = dout.shape[1]
+    rows = T * K + T
+    _dense(what, "dout", dout, torch.float32, (T, d))
+    _dense(what, "topk_gate", topk_gate, torch.float32, (T, K))
+    _need(yq.dim() == 2, f"{what}: yq must be a matrix")
+    _dense(what, "yq", yq, torch.uint8, (yq.shape[0], d))
+    _dense(what, "ys", ys, torch.float32, (yq.shape[0], d // 128))
+    dev = _here(what, dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate, dev_err)
+    dyq = torch.empty(rows, d, dtype=torch.uint8, device=dev) if dyq is None else dyq
+    dys = torch.empty(rows, d // 128, dtype=torch.float32, device=dev) if dys is None else dys
+    dgate = torch.empty(T, K, dtype=torch.float32, device=dev) if dgate is None else dgate
+    if want_dy and dy is None:
+        dy = torch.empty(rows, d, dtype=torch.float32, device=dev)
+    _dense(what, "dyq", dyq, torch.uint8, (rows, d))
+    _dense(what, "dys", dys, torch.float32, (rows, d // 128))
+    _dense(what, "dgate", dgate, torch.float32, (T, K))
+    if dy is not None:
+        _dense(what, "dy", dy, torch.float32, (rows, d))
+    _count(what)
+    _check(lib().moe_combine_checkpoint_backward(
+        dout.data_ptr(), dst_of.data_ptr(), topk_gate.data_ptr(), yq.data_ptr(), ys.data_ptr(),
+        yq.shape[0], T, K, d, dyq.data_ptr(), dys.data_ptr(), _ptr(dy), dgate.data_ptr(),
+        _ptr(dev_err), _stream(stream)), what)
+    return dyq, dys, dy, dgate
+
+
+# ------------------------------------------------------- router's gradient ---
+def moe_route_backward_workspace_size(T, d, E) -> int:
+    n = _sz(0)
+    _check(lib().moe_route_backward_workspace_size(T, d, E, ctypes.byref(n)),
+           "moe_route_backward_workspace_size")
+    return n.value
+
+
+def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base=None, f=None,
+                       dloss=None, alpha=1e-4, seq_len=0, dlogits=None, du=None, dcentroids=None,
+                       ws=None, want_dcentroids=True, dev_err=None, stream=None):
+    """The router's gradient from dgate fp32 [T][K] (or None) and, with f
+    fp32 [T/seq_len][E], from the balance loss's upstream gradient dloss fp32
+    [T/seq_len] (None: ones).  Returns (dlogits fp32 [T][E], du fp32 [T][d] =
+    du_base + dlogits . centroids, dcentroids fp32 [E][d] or None); du may be
+    du_base."""
+    what = "moe_route_backward"
+    _need(logits.dim() == 2 and u.dim() == 2, f"{what}: logits and u must be matrices")
+    T, E = logits.shape
+    d = u.shape[1]
+    _need(topk_idx.dim() == 2, f"{what}: topk_idx must be [T][K]")
+    K = topk_idx.shape[1]
+    f32 = torch.float32
+    _dense(what, "logits", logits, f32, (T, E))
+    _dense(what, "topk_idx", topk_idx, torch.int32, (T, K))
+    _dense(what, "topk_gate", topk_gate, f32, (T, K))
+    ldu = _rows2d(what, "u", u, d, T, torch.bfloat16)
+    _dense(what, "centroids", centroids, torch.bfloat16, (E, d))
+    if dgate is not None:
+        _dense(what, "dgate", dgate, f32, (T, K))
+    if f is not None:
+        _need(seq_len > 0 and T % seq_len == 0, f"{what}: T must be a multiple of seq_len")
+        _dense(what, "f", f, f32, (T // seq_len, E))
+        if dloss is not None:
+            _dense(what, "dloss", dloss, f32, (T // seq_len,))
+    if du_base is not None:
+        _dense(what, "du_base", du_base, f32, (T, d))
+    dev = _here(what, dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f, dloss, dlogits,
+                du, dcentroids, ws, dev_err)
+    dlogits = torch.empty(T, E, dtype=f32, device=dev) if dlogits is None else dlogits
+    du = torch.empty(T, d, dtype=f32, device=dev) if du is None else du
+    if want_dcentroids and dcentroids is None:
+        dcentroids = torch.empty(E, d, dtype=f32, device=dev)
+    _dense(what, "dlogits", dlogits, f32, (T, E))
+    _dense(what, "du", du, f32, (T, d))
+    if dcentroids is not None:
+        _dense(what, "dcentroids", dcentroids, f32, (E, d))
+    if ws is None:
+        ws = torch.empty(max(moe_route_backward_workspace_size(T, d, E), 16), dtype=torch.uint8,
+                         device=dev)
+    _count(what)
+    _check(lib().moe_route_backward(
+        _ptr(dgate), logits.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), u.data_ptr(), ldu,
+        centroids.data_ptr(), T, d, E, K, _ptr(f), _ptr(dloss), int(seq_len), float(alpha),
+        _ptr(du_base), dlogits.data_ptr(), du.data_ptr(), _ptr(dcentroids), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _ptr(dev_err), _stream(stream)), what)
+    return dlogits, du, dcentroids

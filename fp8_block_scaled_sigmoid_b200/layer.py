@@ -44,12 +44,13 @@ def reduce_load_counts(counts: torch.Tensor, tokens_per_rank: int, process_group
 
 
 def reduce_weight_grads(grads: dict, process_group=None) -> dict:
-    """Data parallelism: sum the fp32 expert weight gradients (dW1, dW2) over
-    the ranks in place, so every rank holds the gradient of the whole batch."""
+    """Data parallelism: sum the fp32 expert weight gradients (dW1, dW2) and
+    the centroids' (dcentroids) over the ranks in place, so every rank holds
+    the gradient of the whole batch."""
     if process_group is None:
         return grads
     import torch.distributed as dist
-    for k in ("dW1", "dW2"):
+    for k in ("dW1", "dW2", "dcentroids"):
         if k in grads:
             dist.all_reduce(grads[k], op=dist.ReduceOp.SUM, group=process_group)
     return grads
@@ -100,13 +101,20 @@ class MoELayer:
     ``pow2`` selects the power-of-two scale variant: the activations and h are
     quantised with scales rounded up to powers of two and both expert GEMMs
     hand the scales to the tensor core (grouped_gemm_fp8_pow2); the weights
-    must come from make_fp8_weights(..., pow2=True)."""
+    must come from make_fp8_weights(..., pow2=True).
+
+    ``router_grad`` makes forward_train keep what the router's gradient needs
+    (the logits, and the expert outputs as an 8-bit checkpoint) and backward
+    include the router: du then holds its share too, and the centroids'
+    gradient is returned."""
 
     def __init__(self, cfg: MoEConfig, centroids: torch.Tensor, bias: torch.Tensor,
                  w1q, w1s, w2q, w2s, T: int | None = None, process_group=None,
                  keep_logits: bool = False, pow2: bool = False, balance_loss: bool = False,
-                 seq_len: int | None = None, alpha: float = 1e-4):
+                 seq_len: int | None = None, alpha: float = 1e-4, router_grad: bool = False):
         self.cfg = cfg
+        self.router_grad = router_grad
+        keep_logits = keep_logits or router_grad
         self.pow2 = pow2
         self.T = cfg.T if T is None else T
         self.dev = centroids.device
@@ -215,7 +223,9 @@ class MoELayer:
         input gu in FP8 (1x128 tiles; "Low-Precision Activation"), besides the
         FP8 expert inputs Xq and the routing that forward() keeps anyway.
         GEMM 1 writes gu in fp32, which is quantised for the cache and
-        through SwiGLU for h."""
+        through SwiGLU for h.  With router_grad also the logits, the 8-bit
+        checkpoint of the expert outputs, and u itself (not copied: it must
+        keep its values until backward)."""
         assert u.shape == (self.T, self.cfg.d) and u.dtype == torch.bfloat16
         c = self.cfg
         rows = self.pairs + self.T
@@ -235,10 +245,25 @@ class MoELayer:
         _abi.fp8_quant_1x128_f32(self.GU, self.pow2, self.GUq, self.GUs)
         _abi.swiglu_quant(self.GU, c.I, self.H, self.Hs, pow2=self.pow2)
         self.step_gemm2()
-        self.step_combine(u, self.out)
+        if self.router_grad:
+            self.step_combine_checkpoint(u)
+            self._u_train = u
+        else:
+            self.step_combine(u, self.out)
         if update_bias:
             self.step_bias_update()
         return self.out
+
+    def step_combine_checkpoint(self, u):
+        """The combine that also leaves the routed expert outputs in 8 bits
+        (Yq, Ys), which is all the backward needs of Y."""
+        P = self.pairs
+        if getattr(self, "Yq", None) is None:
+            self.Yq = torch.empty(P, self.cfg.d, dtype=torch.uint8, device=self.dev)
+            self.Ys = torch.empty(P, self.cfg.d // 128, dtype=torch.float32, device=self.dev)
+        _abi.moe_combine_checkpoint(self.Y[:P], self.perm["dst_of"], self.gate, self.Y[P:], u,
+                                    self.out, self.Yq, self.Ys, pow2=self.pow2,
+                                    dev_err=self.dev_err)
 
     def transposed_weights(self):
         """The Dgrad GEMMs' B operands: W1^T [G][d][2I] and W2^T [G][I][d]
@@ -249,11 +274,16 @@ class MoELayer:
             self._wt = (w1t, w1ts, w2t, w2ts)
         return self._wt
 
-    def backward(self, dout: torch.Tensor, weight_grads: bool = True, mark=None) -> dict:
+    def backward(self, dout: torch.Tensor, weight_grads: bool = True, mark=None,
+                 dbalance: torch.Tensor | None = None) -> dict:
         """Gradients of the expert FFNs for the upstream gradient dout (fp32
         [T][d]) of the last forward_train: du (the layer input's gradient
-        through the residual and the experts; the router's share is not
-        included), and with weight_grads dW1 [G][2I][d], dW2 [G][d][I].
+        through the residual and the experts; with router_grad through the
+        router as well), and with weight_grads dW1 [G][2I][d], dW2 [G][d][I].
+        With router_grad also dgate [T][K], dlogits [T][E] and (weight_grads)
+        dcentroids [E][d]; dbalance (fp32, one value per sequence) is the
+        upstream gradient of the balance loss of a layer built with
+        balance_loss, None where the loss is not trained.
         Dgrad: dy (1x128 FP8) . W2 -> dh; SwiGLU backward on the cached FP8
         gu -> dgu (1x128 FP8); dgu . W1 -> dx; un-permute.  Wgrad: the
         token-major 128x1 operands dy^T, h^T (recomputed), dgu^T, x^T through
@@ -261,8 +291,16 @@ class MoELayer:
         c = self.cfg
         p = self.perm
         mark = mark or (lambda name: None)
+        if dbalance is not None and not (self.router_grad and self.balance is not None):
+            raise _abi.MoEError("backward: dbalance needs a layer built with router_grad and balance_loss")
         w1t, w1ts, w2t, w2ts = self.transposed_weights()
-        dyq, dys, dy = _abi.moe_combine_backward(dout, p["dst_of"], self.gate, want_dy=weight_grads)
+        dgate = None
+        if self.router_grad:
+            dyq, dys, dy, dgate = _abi.moe_combine_checkpoint_backward(
+                dout, p["dst_of"], self.gate, self.Yq, self.Ys, want_dy=weight_grads,
+                dev_err=self.dev_err)
+        else:
+            dyq, dys, dy = _abi.moe_combine_backward(dout, p["dst_of"], self.gate, want_dy=weight_grads)
         mark("combine_backward")
         dh = _abi.grouped_gemm_fp8_blockscaled(dyq, dys, w2t, w2ts, p["offsets"], p["tile_group"],
                                                p["tile_start"], p["n_tiles"], self.max_tiles,
@@ -276,7 +314,21 @@ class MoELayer:
         mark("dgrad1")
         du = _abi.moe_unpermute_add(dx, p["dst_of"], dout)
         mark("unpermute")
+        dlogits = dcentroids = None
+        if self.router_grad:
+            b = self.balance
+            with_balance = dbalance is not None
+            dlogits, du, dcentroids = _abi.moe_route_backward(
+                dgate, self.logits, self.idx, self.gate, self._u_train, self.centroids, du_base=du,
+                du=du, f=b.f[:b.n_seq] if with_balance else None, dloss=dbalance,
+                alpha=b.alpha if with_balance else 0.0, seq_len=b.seq_len if with_balance else 0,
+                want_dcentroids=weight_grads, dev_err=self.dev_err)
+            mark("route_backward")
         r = {"du": du, "dyq": dyq, "dys": dys, "dh": dh, "dguq": dguq, "dgus": dgus, "dx": dx}
+        if self.router_grad:
+            r.update({"dgate": dgate, "dlogits": dlogits})
+            if weight_grads:
+                r["dcentroids"] = dcentroids
         if weight_grads:
             G = c.E + c.n_shared
             tabs = (p["offsets"], p["tile_group"], p["tile_start"], p["n_tiles"], self.max_tiles)

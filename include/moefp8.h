@@ -59,6 +59,9 @@ typedef enum {
   MOE_EP_SWIGLU_QUANT = 1 /* D is E4M3 [rows][N/2] with d_scale fp32 [rows][N/256] */
 } moe_epilogue;
 
+/* Element type of the 16/32-bit rows that moe_sort_rows and its kin move. */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
 /* Codes the kernels write into dev_err. */
 #define MOE_DEVERR_TIMEOUT 1   /* a bounded wait gave up; results are invalid */
 #define MOE_DEVERR_BAD_TABLE 2 /* segment offsets / tile table inconsistent */
@@ -485,6 +488,116 @@ moe_status swiglu_quant_pow2(const float* gu, int rows, int I, uint8_t* h, float
 moe_status moe_combine(const float* Y, const int32_t* dst_of, const float* topk_gate,
                        const float* Y_shared, const uint16_t* u, int T, int K, int d,
                        float* out, moe_stream_t stream);
+
+/* ===========================================================================
+ * Tokens sorted by expert and back in 16 or 32 bits, with both gradients, for
+ * experts that the caller computes itself ([ANN] eq. (12): the routed experts'
+ * outputs weighted by the gates; "No Token-Dropping").  dst_of is
+ * moe_permute_index's table, or any table of distinct rows; a negative entry
+ * is a dropped pair: nothing is written for it, it adds nothing to a sum and
+ * its weight's gradient is 0.  An entry >= rows records MOE_DEVERR_BAD_INDEX
+ * and counts as dropped.  Sorted rows that no pair points at stay as they
+ * were.
+ *   x, out, dx, dout  dtype [T][ld..]     rows of tokens
+ *   xs, y, dxs, dy    dtype [rows][ld..]  rows sorted by expert
+ *   dst_of int32 [T][K];  weight, dweight fp32 [T][K]
+ * Products and sums are fp32 (k ascending), rounded once to dtype; a call's
+ * result does not depend on timing.  No buffer written may overlap one read.
+ * Pointers and leading dimensions need the element's own alignment only
+ * (16-byte aligned rows take the faster path).
+ * Limits: d >= 1, 0 <= K <= 32, ld >= d, rows < 2^31.
+ * =========================================================================== */
+
+/* moe_sort_rows -- xs[dst_of[t][k]] = x[t]. */
+moe_status moe_sort_rows(const void* x, moe_dtype dtype, int64_t ldx, const int32_t* dst_of, int T,
+                         int K, int d, void* xs, int64_t ldxs, int64_t rows, int32_t* dev_err,
+                         moe_stream_t stream);
+
+/* moe_sort_rows_backward -- dx[t] = sum_k dxs[dst_of[t][k]]. */
+moe_status moe_sort_rows_backward(const void* dxs, moe_dtype dtype, int64_t ldxs, int64_t rows,
+                                  const int32_t* dst_of, int T, int K, int d, void* dx, int64_t ldx,
+                                  int32_t* dev_err, moe_stream_t stream);
+
+/* moe_unsort_rows -- out[t] = sum_k weight[t][k] y[dst_of[t][k]]. */
+moe_status moe_unsort_rows(const void* y, moe_dtype dtype, int64_t ldy, int64_t rows,
+                           const int32_t* dst_of, const float* weight, int T, int K, int d,
+                           void* out, int64_t ldo, int32_t* dev_err, moe_stream_t stream);
+
+/* moe_unsort_rows_backward -- dy[dst_of[t][k]] = weight[t][k] dout[t] and
+ * dweight[t][k] = sum_j dout[t][j] y[dst_of[t][k]][j].  dy or dweight may be
+ * NULL (not computed); y is only read for dweight. */
+moe_status moe_unsort_rows_backward(const void* dout, moe_dtype dtype, int64_t ldo, const void* y,
+                                    int64_t ldy, const int32_t* dst_of, const float* weight, int T,
+                                    int K, int d, void* dy, int64_t lddy, int64_t rows,
+                                    float* dweight, int32_t* dev_err, moe_stream_t stream);
+
+/* ===========================================================================
+ * The combine with an 8-bit checkpoint of the expert outputs.  The gates'
+ * gradient, dgate[t][k] = dout[t] . Y[dst_of[t][k]], needs Y in the backward;
+ * the checkpoint keeps it in E4M3 with 1x128 scales (a quarter of the fp32
+ * rows) as [ANN] "Low-Precision Activation" keeps the SwiGLU input.
+ * =========================================================================== */
+
+/* moe_combine_checkpoint -- moe_combine that also leaves the checkpoint:
+ * yq[r], ys[r] = 1x128 quantisation of Y[r] (as fp8_quant_1x128_f32; pow2 != 0
+ * rounds each scale up to a power of two) for every row r = dst_of[t][k].
+ * A negative dst_of adds nothing; one >= rows records MOE_DEVERR_BAD_INDEX
+ * and adds nothing.  Rows of yq / ys that no pair points at stay as they were.
+ *   Y fp32 [rows][d];  yq E4M3 [rows][d];  ys fp32 [rows][d/128];
+ *   the rest as in moe_combine.
+ * Limits: d % 128 == 0, 0 <= K <= 32, rows < 2^31. */
+moe_status moe_combine_checkpoint(const float* Y, int64_t rows, const int32_t* dst_of,
+                                  const float* topk_gate, const float* Y_shared, const uint16_t* u,
+                                  int T, int K, int d, int pow2, float* out, uint8_t* yq, float* ys,
+                                  int32_t* dev_err, moe_stream_t stream);
+
+/* moe_combine_checkpoint_backward -- moe_combine_backward (same dyq, dys and
+ * dy) that also gives the gates' gradient from the checkpoint:
+ *   dgate[t][k] = sum_j dout[t][j] * yq[r][j] * ys[r][j/128],  r = dst_of[t][k]
+ * in fp32 (0 for a negative dst_of).  dyq / dys / dy rows T*K + t are the
+ * shared expert's.  An entry >= min(rows, T*K) records MOE_DEVERR_BAD_INDEX
+ * and counts as dropped.
+ *   yq E4M3 [rows][d], ys fp32 [rows][d/128];  dgate fp32 [T][K]
+ *   dyq, dys, dy (or NULL) as in moe_combine_backward
+ * Limits: d % 128 == 0, 0 <= K <= 32, rows < 2^31, T*K + T < 2^31. */
+moe_status moe_combine_checkpoint_backward(const float* dout, const int32_t* dst_of,
+                                           const float* topk_gate, const uint8_t* yq,
+                                           const float* ys, int64_t rows, int T, int K, int d,
+                                           uint8_t* dyq, float* dys, float* dy, float* dgate,
+                                           int32_t* dev_err, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route_backward -- the router's gradient: through the gates (eq. (13)),
+ * the sigmoid (eq. (15)), the balance loss (eqs. (17)-(20)) and the logits.
+ * With s = Sigmoid(logits), g = topk_gate, s' = s / sum_j s_j:
+ *   dlogits[t][i] = sum over k with topk_idx[t][k] = i of
+ *                     g_k (1 - s_i) (dgate_k - sum_j g_j dgate_j)
+ *                 + s'_i (1 - s_i) (c_i - sum_j s'_j c_j),
+ *   c_i = dloss[q] * alpha * f[q][i] / seq_len  (q the token's sequence),
+ *   du = du_base + dlogits . centroids,   dcentroids = dlogits^T . u
+ * The selection itself (the top-K, the bias, the counts f) has no gradient.
+ *   dgate fp32 [T][K] or NULL (no gate part);  logits fp32 [T][E] (moe_route's
+ *   logits_out);  topk_idx, topk_gate as moe_route wrote them
+ *   f fp32 [T/seq_len][E] or NULL (no balance part; seq_len then unused);
+ *   dloss fp32 [T/seq_len] or NULL (1 for every sequence)
+ *   u bf16 [T][ldu];  centroids bf16 [E][d]
+ *   du_base fp32 [T][d] or NULL (zero); it may be du itself
+ *   dlogits fp32 [T][E], du fp32 [T][d], dcentroids fp32 [E][d], each or NULL
+ *   (not computed);  ws: moe_route_backward_workspace_size() bytes, one call
+ *   at a time
+ * fp32 arithmetic throughout; the result does not depend on timing.  An index
+ * outside [0, E) records MOE_DEVERR_BAD_INDEX and its gate part is left out.
+ * T == 0 sets dcentroids to zero.
+ * Limits: as moe_route (d % 128 == 0, E % 16 == 0, 16 <= E <= 1024, K <= E,
+ * K <= 32), ldu % 8 == 0, T % seq_len == 0.
+ */
+moe_status moe_route_backward_workspace_size(int T, int d, int E, size_t* bytes);
+moe_status moe_route_backward(const float* dgate, const float* logits, const int32_t* topk_idx,
+                              const float* topk_gate, const uint16_t* u, int64_t ldu,
+                              const uint16_t* centroids, int T, int d, int E, int K,
+                              const float* f, const float* dloss, int seq_len, float alpha,
+                              const float* du_base, float* dlogits, float* du, float* dcentroids,
+                              void* ws, size_t ws_bytes, int32_t* dev_err, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_bias_update -- [ANN] "Auxiliary-Loss-Free Load Balancing": after the
