@@ -124,7 +124,7 @@ LAUNCHES_PER_CALL = {"fp8_quant_1x128": 1, "fp8_quant_128x128": 1, "swiglu_quant
                      "moe_seq_balance_loss": 3, "moe_fp8_mma_peak": 1,
                      "moe_sort_rows": 1, "moe_sort_rows_backward": 1, "moe_unsort_rows": 1,
                      "moe_unsort_rows_backward": 1, "moe_combine_checkpoint": 1,
-                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 3}
+                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 4}
 launch_count = 0
 
 
