@@ -115,6 +115,31 @@ def test_backward_without_pairs(cuda_dev):
     assert bool((dyq[:T * K] == 9).all()) and not dgate.any()
 
 
+def test_infinities_and_nan(cuda_dev):
+    """Non-finite values give the same bytes as the framework's quantiser and
+    combine backward on the same rows, and stay in their own rows."""
+    T, K, d = 6, 2, 384
+    y = torch.randn(T * K, d, device=cuda_dev)
+    y[1, 5], y[1, 200], y[4, 300], y[6, 0] = float("inf"), float("nan"), float("-inf"), float("nan")
+    dst = torch.arange(T * K, dtype=torch.int32, device=cuda_dev).view(T, K)
+    g = torch.full((T, K), 0.5, device=cuda_dev)
+    u = torch.randn(T, d, device=cuda_dev).bfloat16()
+    for pow2 in (False, True):
+        out, yq, ys = moe.moe_combine_checkpoint(y, dst, g, None, u, pow2=pow2)
+        q, s = _abi.fp8_quant_1x128_f32(y, pow2=pow2)
+        assert torch.equal(yq, q) and torch.equal(ys.view(torch.int32), s.view(torch.int32))
+        want = moe.moe_combine(y, dst, g, None, u)
+        assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+    dout = torch.randn(T, d, device=cuda_dev)
+    dout[0, 3], dout[1, 100], dout[1, 101], dout[2, 129] = float("inf"), float("nan"), 0.0, float("-inf")
+    dout[3, :128] = 1e-40
+    g[4, 0], g[5, 1] = 0.0, 1e-38
+    dyq, dys, dy, dgate = moe.moe_combine_checkpoint_backward(dout, dst, g, q, s, want_dy=True)
+    q2, s2, y2 = _abi.moe_combine_backward(dout, dst, g, want_dy=True)
+    assert torch.equal(dyq, q2) and torch.equal(dys, s2) and torch.equal(torch.nan_to_num(dy), torch.nan_to_num(y2))
+    assert bool(torch.isfinite(dgate[4:]).all())
+
+
 def test_bad_rows_are_reported_and_skipped(cuda_dev):
     T, K, d = 4, 2, 256
     dst = torch.arange(T * K, dtype=torch.int32, device=cuda_dev).view(T, K)
