@@ -20,26 +20,37 @@
 namespace moe {
 namespace {
 
-constexpr int kCkMaxWarps = 16;
+constexpr int kCkWarps = 4;      // warps of a CTA, each with a piece of its own
+constexpr int kCkMaxWarps = 16;  // most warps of a CTA whose warps share a token
 constexpr int kCkMaxK = 32;
 constexpr int kCkTiles = 4;  // tiles of one warp step
 
-// Warps of a CTA and steps of a warp for a row of so many tiles.
-inline int ck_warps(int tiles) {
+struct Shape {
+  dim3 block;  // (32 * warps of a token, tokens)
+  unsigned grid;
+  size_t smem;
+};
+
+#ifndef VW
+#define VW 4
+#endif
+// Four warps a token where the tokens alone fill the GPU (32 warps an SM),
+// more where they are few, up to 16; several tokens a CTA where a token has
+// fewer pieces.
+Shape ck_shape(int T, int K, int tiles) {
   const int items = (tiles + kCkTiles - 1) / kCkTiles;
-  const int steps = (items + kCkMaxWarps - 1) / kCkMaxWarps;
-  return (items + steps - 1) / steps;
+  const int64_t want = (static_cast<int64_t>(moe_num_sms()) * 32 + T - 1) / T;
+  const int most = static_cast<int>(want < VW ? VW : (want > kCkMaxWarps ? kCkMaxWarps : want));
+  const int steps = (items + most - 1) / most;
+  const int warps = (items + steps - 1) / steps;
+  const int tokens = warps >= 4 ? 1 : 4 / warps;
+  return {dim3(32 * warps, tokens), static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens),
+          static_cast<size_t>(tokens) * warps * K * 8 * sizeof(float)};
 }
 
-__device__ __forceinline__ void codes_to_float(uint32_t w, float (&f)[4]) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
-  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-  const float2 a = __half22float2(__half2(lo));
-  const float2 b = __half22float2(__half2(hi));
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+// Two E4M3 bytes -> two floats (exact: every E4M3 value is a half value).
+__device__ __forceinline__ float2 codes_to_float2(uint32_t w) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
 }
 
 // Largest magnitude of a tile: this lane's 16 values, then its eight lanes.
@@ -53,13 +64,48 @@ __device__ __forceinline__ float tile_amax(const float4 (&v)[4]) {
   return m;
 }
 
+// pow2_ceil(quant_scale(x)) for x >= 1e-4 without the division: 448 = 1.75 *
+// 2^8, so with x = m 2^e the quotient is at most 2^(e-8) when m <= 1.75 (and
+// above 2^(e-9), which rounding cannot undercut), and the next larger m is
+// already rounded above 2^(e-8).  Adding 0x1fffff to the bits carries into the
+// exponent exactly when the mantissa is above 1.75's.
+__device__ __forceinline__ float pow2_quant_scale(float amax) {
+  const float x = fmaxf(amax, kQuantEps);
+  const uint32_t b = ((__float_as_uint(x) + 0x1FFFFFu) & 0x7F800000u) - (8u << 23);
+  return x < INFINITY ? __uint_as_float(b) : x;
+}
+
+// Two fp32 values as one 64-bit register pair: the packed instructions round
+// each half as the single ones do, at half the issue slots.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // The token's pairs, one a lane: sorted row (-1 dropped) and gate.
 __device__ __forceinline__ void load_pair(const int32_t* __restrict__ dst_of,
                                           const float* __restrict__ gate, int64_t t, int K, int lane,
-                                          int64_t rows, int& row, float& g, int32_t* dev_err) {
+                                          int64_t rows, bool live, int& row, float& g,
+                                          int32_t* dev_err) {
   row = -1;
   g = 0.f;
-  if (lane < K) {
+  if (live && lane < K) {
     row = __ldg(dst_of + t * K + lane);
     g = __ldg(gate + t * K + lane);
     if (row >= rows) {
@@ -70,128 +116,164 @@ __device__ __forceinline__ void load_pair(const int32_t* __restrict__ dst_of,
 }
 
 template <bool POW2>
-__global__ void __launch_bounds__(32 * kCkMaxWarps) combine_checkpoint_kernel(
+__global__ void __launch_bounds__(32 * kCkWarps) combine_checkpoint_kernel(
     const float* __restrict__ Y, int64_t rows, const int32_t* __restrict__ dst_of,
     const float* __restrict__ gate, const float* __restrict__ Ysh, const uint16_t* __restrict__ u,
-    int K, int d, float* __restrict__ out, uint8_t* __restrict__ yq, float* __restrict__ ys,
+    int T, int K, int d, float* __restrict__ out, uint8_t* __restrict__ yq, float* __restrict__ ys,
     int32_t* dev_err) {
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tiles = d / 128, items = (tiles + kCkTiles - 1) / kCkTiles;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCkWarps + (threadIdx.x >> 5);
+  const int64_t t = unit / items;
+  if (t >= T) return;
   int row;
   float g;
-  load_pair(dst_of, gate, t, K, lane, rows, row, g, dev_err);
+  load_pair(dst_of, gate, t, K, lane, rows, true, row, g, dev_err);
   const uint32_t kept = __ballot_sync(0xffffffffu, row >= 0);
-  const int tiles = d / 128;
-  for (int item = warp; item * kCkTiles < tiles; item += warps) {
-    const int j = item * kCkTiles + (lane >> 3);
-    const bool in = j < tiles;               // the last step may hold fewer tiles
-    const int64_t col = static_cast<int64_t>(j) * 128 + 4 * (lane & 7);
-    float4 acc[4];
+  const int j = static_cast<int>(unit - t * items) * kCkTiles + (lane >> 3);
+  const bool in = j < tiles;               // a token's last piece may hold fewer tiles
+  const int64_t col = static_cast<int64_t>(j) * 128 + 4 * (lane & 7);
+  float4 acc[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    acc[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      const uint2 ub = __ldg(reinterpret_cast<const uint2*>(u + t * d + col + 32 * s));
+      acc[s] = make_float4(bf16_bits_to_float(ub.x & 0xFFFFu), bf16_bits_to_float(ub.x >> 16),
+                           bf16_bits_to_float(ub.y & 0xFFFFu), bf16_bits_to_float(ub.y >> 16));
+      if (Ysh) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(Ysh + t * d + col + 32 * s));
+        acc[s].x += a.x;
+        acc[s].y += a.y;
+        acc[s].z += a.z;
+        acc[s].w += a.w;
+      }
+    }
+  }
+  float4 next[4];
+  auto fetch = [&](uint32_t left) {
+    const int64_t r = __shfl_sync(0xffffffffu, row, __ffs(left) - 1);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      next[s] = in ? __ldg(reinterpret_cast<const float4*>(Y + r * d + col + 32 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  if (kept) fetch(kept);
+  for (uint32_t left = kept; left;) {
+    const int k = __ffs(left) - 1;
+    left &= left - 1;
+    float4 v[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = next[s];
+    if (left) fetch(left);                 // the next row's loads overlap this row's arithmetic
+    const int64_t r = __shfl_sync(0xffffffffu, row, k);
+    const float w = __shfl_sync(0xffffffffu, g, k);
+    const float s0 = quant_scale(tile_amax(v));
+    const float scale = POW2 ? pow2_ceil(s0) : s0;
+    const float rs = __frcp_rn(scale);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      acc[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in) {
-        const uint2 ub = __ldg(reinterpret_cast<const uint2*>(u + t * d + col + 32 * s));
-        acc[s] = make_float4(bf16_bits_to_float(ub.x & 0xFFFFu), bf16_bits_to_float(ub.x >> 16),
-                             bf16_bits_to_float(ub.y & 0xFFFFu), bf16_bits_to_float(ub.y >> 16));
-        if (Ysh) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(Ysh + t * d + col + 32 * s));
-          acc[s].x += a.x;
-          acc[s].y += a.y;
-          acc[s].z += a.z;
-          acc[s].w += a.w;
-        }
-      }
+      acc[s].x = fmaf(w, v[s].x, acc[s].x);
+      acc[s].y = fmaf(w, v[s].y, acc[s].y);
+      acc[s].z = fmaf(w, v[s].z, acc[s].z);
+      acc[s].w = fmaf(w, v[s].w, acc[s].w);
+      if (in)
+        *reinterpret_cast<uint32_t*>(yq + r * d + col + 32 * s) =
+            e4m3x4(div_by_scale(v[s].x, scale, rs), div_by_scale(v[s].y, scale, rs),
+                   div_by_scale(v[s].z, scale, rs), div_by_scale(v[s].w, scale, rs));
     }
-    float4 next[4];
-    auto fetch = [&](uint32_t left) {
-      const int64_t r = __shfl_sync(0xffffffffu, row, __ffs(left) - 1);
+    if (in && (lane & 7) == 0) ys[r * tiles + j] = scale;
+  }
+  if (in) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        next[s] = in ? __ldg(reinterpret_cast<const float4*>(Y + r * d + col + 32 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    if (kept) fetch(kept);
-    for (uint32_t left = kept; left;) {
-      const int k = __ffs(left) - 1;
-      left &= left - 1;
-      float4 v[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) v[s] = next[s];
-      if (left) fetch(left);                 // the next row's loads overlap this row's arithmetic
-      const int64_t r = __shfl_sync(0xffffffffu, row, k);
-      const float w = __shfl_sync(0xffffffffu, g, k);
-      const float s0 = quant_scale(tile_amax(v));
-      const float scale = POW2 ? pow2_ceil(s0) : s0;
-      const float rs = __frcp_rn(scale);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        acc[s].x = fmaf(w, v[s].x, acc[s].x);
-        acc[s].y = fmaf(w, v[s].y, acc[s].y);
-        acc[s].z = fmaf(w, v[s].z, acc[s].z);
-        acc[s].w = fmaf(w, v[s].w, acc[s].w);
-        if (in)
-          *reinterpret_cast<uint32_t*>(yq + r * d + col + 32 * s) =
-              e4m3x4(div_by_scale(v[s].x, scale, rs), div_by_scale(v[s].y, scale, rs),
-                     div_by_scale(v[s].z, scale, rs), div_by_scale(v[s].w, scale, rs));
-      }
-      if (in && (lane & 7) == 0) ys[r * tiles + j] = scale;
-    }
-    if (in) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) *reinterpret_cast<float4*>(out + t * d + col + 32 * s) = acc[s];
-    }
+    for (int s = 0; s < 4; ++s) *reinterpret_cast<float4*>(out + t * d + col + 32 * s) = acc[s];
   }
 }
 
 // dout is read once a tile and gives all K + 1 gradient tiles.  Its largest
 // magnitude is found once: rounding is monotone, so the largest |fl(g x)| is
-// fl(|g| max |x|).  Power-of-two scales divide exactly, so one product with
-// the inverse gives the quotient.
-__global__ void __launch_bounds__(32 * kCkMaxWarps) combine_checkpoint_backward_kernel(
+// fl(|g| max |x|).  Power-of-two scales divide exactly: a product with the
+// inverse gives the quotient, and folded into the gate it gives the same
+// bits with one product (a gate beyond 1e30 keeps the two).  Without dy a lane
+// holds 16 neighbouring columns, so that a row's codes are one 16-byte access
+// a lane; with it the columns 32 s + 4 l, so that the fp32 rows' are.
+template <bool WITH_DY>
+__global__ void __launch_bounds__(32 * kCkMaxWarps, 2) combine_checkpoint_backward_kernel(
     const float* __restrict__ dout, const int32_t* __restrict__ dst_of,
     const float* __restrict__ gate, const uint8_t* __restrict__ yq, const float* __restrict__ ys,
-    int64_t rows, int64_t P, int K, int d, uint8_t* __restrict__ dyq, float* __restrict__ dys,
+    int64_t rows, int T, int K, int d, uint8_t* __restrict__ dyq, float* __restrict__ dys,
     float* __restrict__ dy, float* __restrict__ dgate, int32_t* dev_err) {
-  __shared__ float dot[kCkMaxWarps][kCkMaxK];
-  const int64_t t = blockIdx.x;
+  extern __shared__ float dot[];  // [tokens][warps][K][8]
+  constexpr int kLane = WITH_DY ? 4 : 16, kStep = WITH_DY ? 32 : 4;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t P = static_cast<int64_t>(T) * K;
   int row;
   float g;
-  load_pair(dst_of, gate, t, K, lane, rows < P ? rows : P, row, g, dev_err);
+  load_pair(dst_of, gate, t, K, lane, rows < P ? rows : P, t < T, row, g, dev_err);
   const uint32_t kept = __ballot_sync(0xffffffffu, row >= 0);
   const int tiles = d / 128;
-  dot[warp][lane] = 0.f;
-  __syncwarp();
-  for (int item = warp; item * kCkTiles < tiles; item += warps) {
+  bool first = true;
+  for (int item = warp; item * kCkTiles < tiles && t < T; item += warps) {
     const int j = item * kCkTiles + (lane >> 3);
     const bool in = j < tiles;
-    const int64_t col = static_cast<int64_t>(j) * 128 + 4 * (lane & 7);
+    const int64_t col = static_cast<int64_t>(j) * 128 + kLane * (lane & 7);
     float4 a[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      a[s] = in ? __ldg(reinterpret_cast<const float4*>(dout + t * d + col + 32 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    uint32_t next[4];
+      a[s] = in ? __ldg(reinterpret_cast<const float4*>(dout + t * d + col + kStep * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    uint4 next = make_uint4(0u, 0u, 0u, 0u);
     float next_scale = 0.f;
     auto fetch = [&](uint32_t left) {
-      const int64_t r = __shfl_sync(0xffffffffu, row, __ffs(left) - 1);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        next[s] = in ? __ldg(reinterpret_cast<const uint32_t*>(yq + r * d + col + 32 * s)) : 0u;
-      next_scale = in ? __ldg(ys + r * tiles + j) : 0.f;
+      const int r = __shfl_sync(0xffffffffu, row, __ffs(left) - 1);
+      if (!in) return;
+      const uint8_t* p = yq + static_cast<int64_t>(r) * d + col;
+      if (WITH_DY)
+        next = make_uint4(__ldg(reinterpret_cast<const uint32_t*>(p)), __ldg(reinterpret_cast<const uint32_t*>(p + 32)),
+                          __ldg(reinterpret_cast<const uint32_t*>(p + 64)), __ldg(reinterpret_cast<const uint32_t*>(p + 96)));
+      else
+        next = __ldg(reinterpret_cast<const uint4*>(p));
+      next_scale = __ldg(ys + static_cast<int64_t>(r) * tiles + j);
     };
     if (kept) fetch(kept);
     const float amax = tile_amax(a);
-    auto write_row = [&](int64_t r, float w) {
-      const float scale = pow2_ceil(quant_scale(__fmul_rn(fabsf(w), amax)));
-      // an infinite maximum leaves no finite scale: every code is NaN
-      const float inv = scale < INFINITY ? __frcp_rn(scale) : NAN;
+    uint64_t a2[8];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float4 v = make_float4(__fmul_rn(w, a[s].x), __fmul_rn(w, a[s].y), __fmul_rn(w, a[s].z),
-                                     __fmul_rn(w, a[s].w));
-        *reinterpret_cast<uint32_t*>(dyq + r * d + col + 32 * s) =
-            e4m3x4(__fmul_rn(v.x, inv), __fmul_rn(v.y, inv), __fmul_rn(v.z, inv), __fmul_rn(v.w, inv));
-        if (dy) *reinterpret_cast<float4*>(dy + r * d + col + 32 * s) = v;
+    for (int s = 0; s < 4; ++s) {
+      a2[2 * s] = pack2(a[s].x, a[s].y);
+      a2[2 * s + 1] = pack2(a[s].z, a[s].w);
+    }
+    auto write_row = [&](int64_t r, float w) {
+      const float scale = pow2_quant_scale(__fmul_rn(fabsf(w), amax));
+      // 1 / 2^e by its exponent; an infinite maximum leaves no finite scale: every code is NaN
+      const float inv = scale < INFINITY ? __uint_as_float(0x7F000000u - __float_as_uint(scale)) : NAN;
+      uint32_t q[4];
+      if (!WITH_DY && fabsf(w) <= 1e30f) {
+        const float wi = __fmul_rn(w, inv);
+        const uint64_t wi2 = pack2(wi, wi);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float2 ql = unpack2(mul2(wi2, a2[2 * s])), qh = unpack2(mul2(wi2, a2[2 * s + 1]));
+          q[s] = e4m3x4(ql.x, ql.y, qh.x, qh.y);
+        }
+      } else {
+        const uint64_t w2 = pack2(w, w), inv2 = pack2(inv, inv);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint64_t lo = mul2(w2, a2[2 * s]), hi = mul2(w2, a2[2 * s + 1]);
+          const float2 ql = unpack2(mul2(lo, inv2)), qh = unpack2(mul2(hi, inv2));
+          q[s] = e4m3x4(ql.x, ql.y, qh.x, qh.y);
+          if (WITH_DY) {
+            const float2 vl = unpack2(lo), vh = unpack2(hi);
+            *reinterpret_cast<float4*>(dy + r * d + col + kStep * s) = make_float4(vl.x, vl.y, vh.x, vh.y);
+          }
+        }
+      }
+      uint8_t* p = dyq + r * d + col;
+      if (WITH_DY) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) *reinterpret_cast<uint32_t*>(p + 32 * s) = q[s];
+      } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
       }
       if ((lane & 7) == 0) dys[r * tiles + j] = scale;
     };
@@ -199,31 +281,39 @@ __global__ void __launch_bounds__(32 * kCkMaxWarps) combine_checkpoint_backward_
     for (uint32_t left = kept; left;) {
       const int k = __ffs(left) - 1;
       left &= left - 1;
-      uint32_t code[4];
+      const uint32_t code[4] = {next.x, next.y, next.z, next.w};
       const float scale = next_scale;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) code[s] = next[s];
       if (left) fetch(left);
-      const int64_t r = __shfl_sync(0xffffffffu, row, k);
+      const int r = __shfl_sync(0xffffffffu, row, k);
       const float w = __shfl_sync(0xffffffffu, g, k);
       if (in) write_row(r, w);
-      float p = 0.f;
+      uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        float f[4];
-        codes_to_float(code[s], f);
-        p = fmaf(a[s].w, f[3], fmaf(a[s].z, f[2], fmaf(a[s].y, f[1], fmaf(a[s].x, f[0], p))));
+        const float2 fl = codes_to_float2(code[s] & 0xFFFFu), fh = codes_to_float2(code[s] >> 16);
+        sum2 = fma2(a2[2 * s], pack2(fl.x, fl.y), sum2);
+        sum2 = fma2(a2[2 * s + 1], pack2(fh.x, fh.y), sum2);
       }
-      p = __fmul_rn(p, scale);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) p += __shfl_xor_sync(0xffffffffu, p, off);
-      if (lane == 0) dot[warp][k] += p;
+      const float2 sum = unpack2(sum2);
+      float p = __fmul_rn(__fadd_rn(sum.x, sum.y), scale);
+      // the rest of the sum over the lanes is left to the end
+      p += __shfl_xor_sync(0xffffffffu, p, 16);
+      p += __shfl_xor_sync(0xffffffffu, p, 8);
+      if (lane < 8) {
+        float* at = dot + ((threadIdx.y * warps + warp) * K + k) * 8 + lane;
+        *at = first ? p : *at + p;
+      }
     }
+    first = false;
   }
   __syncthreads();
-  if (threadIdx.x < K) {
+  if (t < T && threadIdx.x < K) {
     float sum = 0.f;
-    for (int w = 0; w < warps; ++w) sum += dot[w][threadIdx.x];
+    if ((kept >> threadIdx.x) & 1u) {
+      for (int w = 0; w < warps; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += dot[((threadIdx.y * warps + w) * K + threadIdx.x) * 8 + i];
+    }
     dgate[t * K + threadIdx.x] = sum;
   }
 }
@@ -250,8 +340,11 @@ extern "C" moe_status moe_combine_checkpoint(const float* Y, int64_t rows, const
       !aligned4(ys) || !aligned4(dst_of) || !aligned4(topk_gate))
     return MOE_ERR_ALIGN;
   auto kern = pow2 ? combine_checkpoint_kernel<true> : combine_checkpoint_kernel<false>;
-  kern<<<T, 32 * ck_warps(d / 128), 0, static_cast<cudaStream_t>(stream)>>>(
-      Y, rows, dst_of, topk_gate, Y_shared, u, K, d, out, yq, ys, dev_err);
+  const int64_t items = (d / 128 + kCkTiles - 1) / kCkTiles;
+  const int64_t blocks = (T * items + kCkWarps - 1) / kCkWarps;
+  if (blocks > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(blocks), 32 * kCkWarps, 0, static_cast<cudaStream_t>(stream)>>>(
+      Y, rows, dst_of, topk_gate, Y_shared, u, T, K, d, out, yq, ys, dev_err);
   MOE_CUDA_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -274,8 +367,10 @@ extern "C" moe_status moe_combine_checkpoint_backward(const float* dout, const i
   if (!aligned16(dout) || !aligned16(yq) || !aligned16(dyq) || !aligned16(dy) || !aligned4(ys) ||
       !aligned4(dys) || !aligned4(dgate) || !aligned4(dst_of) || !aligned4(topk_gate))
     return MOE_ERR_ALIGN;
-  combine_checkpoint_backward_kernel<<<T, 32 * ck_warps(d / 128), 0, static_cast<cudaStream_t>(stream)>>>(
-      dout, dst_of, topk_gate, yq, ys, rows, P, K, d, dyq, dys, dy, dgate, dev_err);
+  const Shape sh = ck_shape(T, K, d / 128);
+  auto kern = dy ? combine_checkpoint_backward_kernel<true> : combine_checkpoint_backward_kernel<false>;
+  kern<<<sh.grid, sh.block, sh.smem, static_cast<cudaStream_t>(stream)>>>(
+      dout, dst_of, topk_gate, yq, ys, rows, T, K, d, dyq, dys, dy, dgate, dev_err);
   MOE_CUDA_CHECK_LAUNCH();
   return MOE_OK;
 }
