@@ -124,7 +124,7 @@ LAUNCHES_PER_CALL = {"fp8_quant_1x128": 1, "fp8_quant_128x128": 1, "swiglu_quant
                      "moe_seq_balance_loss": 3, "moe_fp8_mma_peak": 1,
                      "moe_sort_rows": 1, "moe_sort_rows_backward": 1, "moe_unsort_rows": 1,
                      "moe_unsort_rows_backward": 1, "moe_combine_checkpoint": 1,
-                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 4}
+                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 3}
 launch_count = 0
 
 
@@ -644,54 +644,59 @@ def grouped_gemm_fp8_wgrad(At, a_atoms, Bt, b_atoms, tile_start, groups, dW=None
 
 
 # --------------------------------------- tokens sorted by expert and back ---
+# A small call costs less than its checks if those are careless: no message is
+# formatted and no Stream or device object is made unless something is wrong.
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise MoEError(what)
-
-
-def _here(what: str, *tensors) -> torch.device:
-    """The device of the tensors (None skipped): one device for all of them,
-    and the current one, whose stream the call is queued on."""
-    dev = None
+def _queue(what, stream, *tensors) -> int:
+    """The stream to queue on, after checking that all tensors (None skipped)
+    are on one device and that it is the current one."""
+    dev = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        _need(t.is_cuda, f"{what}: expected a CUDA tensor")
-        dev = t.device if dev is None else dev
-        _need(t.device == dev, f"{what}: tensors on different devices")
-    _need(dev.index == torch.cuda.current_device(),
-          f"{what}: the tensors are not on the current device")
-    return dev
+        if t is not None and t.get_device() != dev:
+            raise MoEError(f"{what}: every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _rows2d(what: str, name: str, t, d=None, n=None, dtype=None):
-    """Checks a matrix of contiguous rows (any row stride >= d)."""
-    _need(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1),
-          f"{what}: {name} must be a matrix with contiguous rows")
-    _need(d is None or t.shape[1] == d, f"{what}: {name} has {t.shape[1]} columns, expected {d}")
-    _need(n is None or t.shape[0] == n, f"{what}: {name} has {t.shape[0]} rows, expected {n}")
-    _need(dtype is None or t.dtype == dtype, f"{what}: {name} must be {dtype}")
-    # the row stride of a single row says nothing
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _dense(what: str, name: str, t, dtype, shape):
-    _need(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          f"{what}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _row_type(what, t) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise MoEError(f"{what}: rows must be bf16, fp16 or fp32, got {t.dtype}")
+    return dt
 
 
-def _table(what: str, dst_of):
-    _need(dst_of.dim() == 2 and dst_of.dtype == torch.int32 and dst_of.is_contiguous(),
-          f"{what}: dst_of must be a contiguous int32 [T][K] table")
+def _ld(what, name, t, rows, d, dtype) -> int:
+    """Row stride of a [rows][d] matrix with contiguous rows (rows None: any)."""
+    n = t.shape[0] if t.dim() == 2 else -1
+    if n < 0 or t.shape[1] != d or (rows is not None and n != rows) or t.dtype != dtype or (
+            t.stride(1) != 1 and d > 1):
+        raise MoEError(f"{what}: {name} must be a {dtype} matrix of {'any number of' if rows is None else rows} "
+                       f"contiguous rows of {d}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    return t.stride(0) if n > 1 else d        # the stride of a single row says nothing
+
+
+def _dense(what, name, t, dtype, shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise MoEError(f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
+                       f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _table(what, dst_of):
+    if dst_of.dim() != 2 or dst_of.dtype != _I32 or not dst_of.is_contiguous():
+        raise MoEError(f"{what}: dst_of must be a contiguous int32 [T][K] table")
     return dst_of.shape
 
 
-def _row_type(what: str, t) -> int:
-    _need(t.dtype in _DTYPES, f"{what}: rows must be bf16, fp16 or fp32")
-    return _DTYPES[t.dtype]
+def _width(what, name, t):
+    if t.dim() != 2:
+        raise MoEError(f"{what}: {name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def moe_sort_rows(x, dst_of, rows=None, out=None, dev_err=None, stream=None):
@@ -701,15 +706,17 @@ def moe_sort_rows(x, dst_of, rows=None, out=None, dev_err=None, stream=None):
     what = "moe_sort_rows"
     T, K = _table(what, dst_of)
     dt = _row_type(what, x)
-    ldx = _rows2d(what, "x", x, n=T)
-    d = x.shape[1]
-    dev = _here(what, x, dst_of, out, dev_err)
+    d = _width(what, "x", x)[1]
+    ldx = _ld(what, "x", x, T, d, x.dtype)
+    st = _queue(what, stream, x, dst_of, out, dev_err)
     if out is None:
-        out = torch.empty(T * K if rows is None else rows, d, dtype=x.dtype, device=dev)
-    ldo = _rows2d(what, "out", out, d, rows, x.dtype)
+        out = x.new_empty((T * K if rows is None else rows, d))
+        ldo = d
+    else:
+        ldo = _ld(what, "out", out, rows, d, x.dtype)
     _count(what)
     _check(lib().moe_sort_rows(x.data_ptr(), dt, ldx, dst_of.data_ptr(), T, K, d, out.data_ptr(),
-                               ldo, out.shape[0], _ptr(dev_err), _stream(stream)), what)
+                               ldo, out.shape[0], _addr(dev_err), st), what)
     return out
 
 
@@ -718,15 +725,17 @@ def moe_sort_rows_backward(dxs, dst_of, dx=None, dev_err=None, stream=None):
     what = "moe_sort_rows_backward"
     T, K = _table(what, dst_of)
     dt = _row_type(what, dxs)
-    lds = _rows2d(what, "dxs", dxs)
-    n, d = dxs.shape
-    dev = _here(what, dxs, dst_of, dx, dev_err)
+    n, d = _width(what, "dxs", dxs)
+    lds = _ld(what, "dxs", dxs, n, d, dxs.dtype)
+    st = _queue(what, stream, dxs, dst_of, dx, dev_err)
     if dx is None:
-        dx = torch.empty(T, d, dtype=dxs.dtype, device=dev)
-    ldx = _rows2d(what, "dx", dx, d, T, dxs.dtype)
+        dx = dxs.new_empty((T, d))
+        ldx = d
+    else:
+        ldx = _ld(what, "dx", dx, T, d, dxs.dtype)
     _count(what)
     _check(lib().moe_sort_rows_backward(dxs.data_ptr(), dt, lds, n, dst_of.data_ptr(), T, K, d,
-                                        dx.data_ptr(), ldx, _ptr(dev_err), _stream(stream)), what)
+                                        dx.data_ptr(), ldx, _addr(dev_err), st), what)
     return dx
 
 
@@ -736,16 +745,18 @@ def moe_unsort_rows(y, dst_of, weight, out=None, dev_err=None, stream=None):
     what = "moe_unsort_rows"
     T, K = _table(what, dst_of)
     dt = _row_type(what, y)
-    ldy = _rows2d(what, "y", y)
-    _dense(what, "weight", weight, torch.float32, (T, K))
-    n, d = y.shape
-    dev = _here(what, y, dst_of, weight, out, dev_err)
+    n, d = _width(what, "y", y)
+    ldy = _ld(what, "y", y, n, d, y.dtype)
+    _dense(what, "weight", weight, _F32, (T, K))
+    st = _queue(what, stream, y, dst_of, weight, out, dev_err)
     if out is None:
-        out = torch.empty(T, d, dtype=y.dtype, device=dev)
-    ldo = _rows2d(what, "out", out, d, T, y.dtype)
+        out = y.new_empty((T, d))
+        ldo = d
+    else:
+        ldo = _ld(what, "out", out, T, d, y.dtype)
     _count(what)
     _check(lib().moe_unsort_rows(y.data_ptr(), dt, ldy, n, dst_of.data_ptr(), weight.data_ptr(), T,
-                                 K, d, out.data_ptr(), ldo, _ptr(dev_err), _stream(stream)), what)
+                                 K, d, out.data_ptr(), ldo, _addr(dev_err), st), what)
     return out
 
 
@@ -758,32 +769,38 @@ def moe_unsort_rows_backward(dout, y, dst_of, weight, dy=None, dweight=None, wan
     what = "moe_unsort_rows_backward"
     T, K = _table(what, dst_of)
     dt = _row_type(what, dout)
-    ldo = _rows2d(what, "dout", dout, n=T)
-    d = dout.shape[1]
-    ldy = _rows2d(what, "y", y, d, dtype=dout.dtype)
-    _dense(what, "weight", weight, torch.float32, (T, K))
-    n = y.shape[0]
-    dev = _here(what, dout, y, dst_of, weight, dy, dweight, dev_err)
-    want_dy, want_dweight = want_dy or dy is not None, want_dweight or dweight is not None
-    _need(want_dy or want_dweight, f"{what}: neither gradient wanted")
-    lddy = 0
-    if want_dy:
-        if dy is None:
-            dy = torch.empty(n, d, dtype=dout.dtype, device=dev)
-        lddy = _rows2d(what, "dy", dy, d, n, dout.dtype)
-    if want_dweight:
-        if dweight is None:
-            dweight = torch.empty(T, K, dtype=torch.float32, device=dev)
-        _dense(what, "dweight", dweight, torch.float32, (T, K))
+    d = _width(what, "dout", dout)[1]
+    ldo = _ld(what, "dout", dout, T, d, dout.dtype)
+    n = _width(what, "y", y)[0]
+    ldy = _ld(what, "y", y, n, d, dout.dtype)
+    _dense(what, "weight", weight, _F32, (T, K))
+    st = _queue(what, stream, dout, y, dst_of, weight, dy, dweight, dev_err)
+    lddy = d
+    if dy is not None:
+        lddy = _ld(what, "dy", dy, n, d, dout.dtype)
+    elif want_dy:
+        dy = dout.new_empty((n, d))
+    if dweight is not None:
+        _dense(what, "dweight", dweight, _F32, (T, K))
+    elif want_dweight:
+        dweight = weight.new_empty((T, K))
+    if dy is None and dweight is None:
+        raise MoEError(f"{what}: neither gradient wanted")
     _count(what)
     _check(lib().moe_unsort_rows_backward(dout.data_ptr(), dt, ldo, y.data_ptr(), ldy,
-                                          dst_of.data_ptr(), weight.data_ptr(), T, K, d, _ptr(dy),
-                                          lddy, n, _ptr(dweight), _ptr(dev_err), _stream(stream)),
-           what)
+                                          dst_of.data_ptr(), weight.data_ptr(), T, K, d, _addr(dy),
+                                          lddy, n, _addr(dweight), _addr(dev_err), st), what)
     return dy, dweight
 
 
 # ------------------------------------------- 8-bit checkpoint of the combine ---
+def _tiled(what, name, t):
+    n, d = _width(what, name, t)
+    if d % 128 != 0:
+        raise MoEError(f"{what}: {name} must have a multiple of 128 columns, got {d}")
+    return n, d
+
+
 def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None, ys=None,
                            pow2=False, dev_err=None, stream=None):
     """moe_combine that also keeps Y in 8 bits: Y fp32 [rows][d] ->
@@ -791,26 +808,30 @@ def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None,
     no pair points at stay as they were (undefined in new buffers)."""
     what = "moe_combine_checkpoint"
     T, K = _table(what, dst_of)
-    _need(Y.dim() == 2, f"{what}: Y must be a matrix")
-    rows, d = Y.shape
-    _need(d % 128 == 0, f"{what}: d must be a multiple of 128")
-    _dense(what, "Y", Y, torch.float32, (rows, d))
-    _dense(what, "topk_gate", topk_gate, torch.float32, (T, K))
-    _dense(what, "u", u, torch.bfloat16, (T, d))
+    rows, d = _tiled(what, "Y", Y)
+    _dense(what, "Y", Y, _F32, (rows, d))
+    _dense(what, "topk_gate", topk_gate, _F32, (T, K))
+    _dense(what, "u", u, _BF16, (T, d))
     if Y_shared is not None:
-        _dense(what, "Y_shared", Y_shared, torch.float32, (T, d))
-    dev = _here(what, Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, dev_err)
-    out = torch.empty(T, d, dtype=torch.float32, device=dev) if out is None else out
-    yq = torch.empty(rows, d, dtype=torch.uint8, device=dev) if yq is None else yq
-    ys = torch.empty(rows, d // 128, dtype=torch.float32, device=dev) if ys is None else ys
-    _dense(what, "out", out, torch.float32, (T, d))
-    _dense(what, "yq", yq, torch.uint8, (rows, d))
-    _dense(what, "ys", ys, torch.float32, (rows, d // 128))
+        _dense(what, "Y_shared", Y_shared, _F32, (T, d))
+    st = _queue(what, stream, Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, dev_err)
+    if out is None:
+        out = Y.new_empty((T, d))
+    else:
+        _dense(what, "out", out, _F32, (T, d))
+    if yq is None:
+        yq = Y.new_empty((rows, d), dtype=_U8)
+    else:
+        _dense(what, "yq", yq, _U8, (rows, d))
+    if ys is None:
+        ys = Y.new_empty((rows, d // 128))
+    else:
+        _dense(what, "ys", ys, _F32, (rows, d // 128))
     _count(what)
     _check(lib().moe_combine_checkpoint(Y.data_ptr(), rows, dst_of.data_ptr(), topk_gate.data_ptr(),
-                                        _ptr(Y_shared), u.data_ptr(), T, K, d, int(bool(pow2)),
-                                        out.data_ptr(), yq.data_ptr(), ys.data_ptr(), _ptr(dev_err),
-                                        _stream(stream)), what)
+                                        _addr(Y_shared), u.data_ptr(), T, K, d, int(bool(pow2)),
+                                        out.data_ptr(), yq.data_ptr(), ys.data_ptr(),
+                                        _addr(dev_err), st), what)
     return out, yq, ys
 
 
@@ -820,31 +841,34 @@ def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, d
     dys [T*K+T][d/128], dy fp32 or None, dgate fp32 [T][K])."""
     what = "moe_combine_checkpoint_backward"
     T, K = _table(what, dst_of)
-    _need(dout.dim() == 2 and dout.shape[0] == T and dout.shape[1] % 128 == 0,
-          f"{what}: dout must be [T][d] with d a multiple of 128")
-    d = dout.shape[1]
+    d = _tiled(what, "dout", dout)[1]
     rows = T * K + T
-    _dense(what, "dout", dout, torch.float32, (T, d))
-    _dense(what, "topk_gate", topk_gate, torch.float32, (T, K))
-    _need(yq.dim() == 2, f"{what}: yq must be a matrix")
-    _dense(what, "yq", yq, torch.uint8, (yq.shape[0], d))
-    _dense(what, "ys", ys, torch.float32, (yq.shape[0], d // 128))
-    dev = _here(what, dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate, dev_err)
-    dyq = torch.empty(rows, d, dtype=torch.uint8, device=dev) if dyq is None else dyq
-    dys = torch.empty(rows, d // 128, dtype=torch.float32, device=dev) if dys is None else dys
-    dgate = torch.empty(T, K, dtype=torch.float32, device=dev) if dgate is None else dgate
-    if want_dy and dy is None:
-        dy = torch.empty(rows, d, dtype=torch.float32, device=dev)
-    _dense(what, "dyq", dyq, torch.uint8, (rows, d))
-    _dense(what, "dys", dys, torch.float32, (rows, d // 128))
-    _dense(what, "dgate", dgate, torch.float32, (T, K))
+    n = _width(what, "yq", yq)[0]
+    _dense(what, "dout", dout, _F32, (T, d))
+    _dense(what, "topk_gate", topk_gate, _F32, (T, K))
+    _dense(what, "yq", yq, _U8, (n, d))
+    _dense(what, "ys", ys, _F32, (n, d // 128))
+    st = _queue(what, stream, dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate, dev_err)
+    if dyq is None:
+        dyq = yq.new_empty((rows, d))
+    else:
+        _dense(what, "dyq", dyq, _U8, (rows, d))
+    if dys is None:
+        dys = dout.new_empty((rows, d // 128))
+    else:
+        _dense(what, "dys", dys, _F32, (rows, d // 128))
+    if dgate is None:
+        dgate = dout.new_empty((T, K))
+    else:
+        _dense(what, "dgate", dgate, _F32, (T, K))
     if dy is not None:
-        _dense(what, "dy", dy, torch.float32, (rows, d))
+        _dense(what, "dy", dy, _F32, (rows, d))
+    elif want_dy:
+        dy = dout.new_empty((rows, d))
     _count(what)
     _check(lib().moe_combine_checkpoint_backward(
-        dout.data_ptr(), dst_of.data_ptr(), topk_gate.data_ptr(), yq.data_ptr(), ys.data_ptr(),
-        yq.shape[0], T, K, d, dyq.data_ptr(), dys.data_ptr(), _ptr(dy), dgate.data_ptr(),
-        _ptr(dev_err), _stream(stream)), what)
+        dout.data_ptr(), dst_of.data_ptr(), topk_gate.data_ptr(), yq.data_ptr(), ys.data_ptr(), n, T,
+        K, d, dyq.data_ptr(), dys.data_ptr(), _addr(dy), dgate.data_ptr(), _addr(dev_err), st), what)
     return dyq, dys, dy, dgate
 
 
@@ -865,43 +889,44 @@ def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base
     du_base + dlogits . centroids, dcentroids fp32 [E][d] or None); du may be
     du_base."""
     what = "moe_route_backward"
-    _need(logits.dim() == 2 and u.dim() == 2, f"{what}: logits and u must be matrices")
-    T, E = logits.shape
-    d = u.shape[1]
-    _need(topk_idx.dim() == 2, f"{what}: topk_idx must be [T][K]")
-    K = topk_idx.shape[1]
-    f32 = torch.float32
-    _dense(what, "logits", logits, f32, (T, E))
-    _dense(what, "topk_idx", topk_idx, torch.int32, (T, K))
-    _dense(what, "topk_gate", topk_gate, f32, (T, K))
-    ldu = _rows2d(what, "u", u, d, T, torch.bfloat16)
-    _dense(what, "centroids", centroids, torch.bfloat16, (E, d))
+    T, E = _width(what, "logits", logits)
+    d = _width(what, "u", u)[1]
+    K = _width(what, "topk_idx", topk_idx)[1]
+    _dense(what, "logits", logits, _F32, (T, E))
+    _dense(what, "topk_idx", topk_idx, _I32, (T, K))
+    _dense(what, "topk_gate", topk_gate, _F32, (T, K))
+    ldu = _ld(what, "u", u, T, d, _BF16)
+    _dense(what, "centroids", centroids, _BF16, (E, d))
     if dgate is not None:
-        _dense(what, "dgate", dgate, f32, (T, K))
+        _dense(what, "dgate", dgate, _F32, (T, K))
     if f is not None:
-        _need(seq_len > 0 and T % seq_len == 0, f"{what}: T must be a multiple of seq_len")
-        _dense(what, "f", f, f32, (T // seq_len, E))
+        if seq_len <= 0 or T % seq_len != 0:
+            raise MoEError(f"{what}: T = {T} must be a multiple of seq_len = {seq_len}")
+        _dense(what, "f", f, _F32, (T // seq_len, E))
         if dloss is not None:
-            _dense(what, "dloss", dloss, f32, (T // seq_len,))
+            _dense(what, "dloss", dloss, _F32, (T // seq_len,))
     if du_base is not None:
-        _dense(what, "du_base", du_base, f32, (T, d))
-    dev = _here(what, dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f, dloss, dlogits,
-                du, dcentroids, ws, dev_err)
-    dlogits = torch.empty(T, E, dtype=f32, device=dev) if dlogits is None else dlogits
-    du = torch.empty(T, d, dtype=f32, device=dev) if du is None else du
-    if want_dcentroids and dcentroids is None:
-        dcentroids = torch.empty(E, d, dtype=f32, device=dev)
-    _dense(what, "dlogits", dlogits, f32, (T, E))
-    _dense(what, "du", du, f32, (T, d))
+        _dense(what, "du_base", du_base, _F32, (T, d))
+    st = _queue(what, stream, dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f, dloss,
+                dlogits, du, dcentroids, ws, dev_err)
+    if dlogits is None:
+        dlogits = logits.new_empty((T, E))
+    else:
+        _dense(what, "dlogits", dlogits, _F32, (T, E))
+    if du is None:
+        du = logits.new_empty((T, d))
+    else:
+        _dense(what, "du", du, _F32, (T, d))
     if dcentroids is not None:
-        _dense(what, "dcentroids", dcentroids, f32, (E, d))
+        _dense(what, "dcentroids", dcentroids, _F32, (E, d))
+    elif want_dcentroids:
+        dcentroids = logits.new_empty((E, d))
     if ws is None:
-        ws = torch.empty(max(moe_route_backward_workspace_size(T, d, E), 16), dtype=torch.uint8,
-                         device=dev)
+        ws = logits.new_empty(moe_route_backward_workspace_size(T, d, E), dtype=_U8)
     _count(what)
     _check(lib().moe_route_backward(
-        _ptr(dgate), logits.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), u.data_ptr(), ldu,
-        centroids.data_ptr(), T, d, E, K, _ptr(f), _ptr(dloss), int(seq_len), float(alpha),
-        _ptr(du_base), dlogits.data_ptr(), du.data_ptr(), _ptr(dcentroids), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _ptr(dev_err), _stream(stream)), what)
+        _addr(dgate), logits.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), u.data_ptr(), ldu,
+        centroids.data_ptr(), T, d, E, K, _addr(f), _addr(dloss), seq_len, alpha, _addr(du_base),
+        dlogits.data_ptr(), du.data_ptr(), _addr(dcentroids), ws.data_ptr(), ws.nbytes,
+        _addr(dev_err), st), what)
     return dlogits, du, dcentroids

@@ -61,6 +61,21 @@ bool moe_make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt
   return r == CUDA_SUCCESS;
 }
 
+bool moe_make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                      const uint64_t (&extent)[3], const uint64_t (&stride_bytes)[2],
+                      const uint32_t (&box)[3], int swizzle_bytes) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {extent[0], extent[1], extent[2]};
+  const cuuint64_t strides[2] = {stride_bytes[0], stride_bytes[1]};
+  const cuuint32_t boxes[3] = {box[0], box[1], box[2]};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, dtype, 3, const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int moe_num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;

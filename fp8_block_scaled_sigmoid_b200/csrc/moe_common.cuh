@@ -99,6 +99,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 3-D tile; c0 innermost.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
                                                  int32_t c0, int32_t c1, uint64_t policy) {
   asm volatile(
@@ -329,6 +339,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
 bool moe_make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                       uint64_t inner_elems, uint64_t outer_rows, uint64_t row_stride_bytes,
                       uint32_t box_inner, uint32_t box_outer, int swizzle_bytes = 128);
+
+// The same for a 3-D tensor (extents and box innermost first, 64- or 128-byte swizzle).
+bool moe_make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                      const uint64_t (&extent)[3], const uint64_t (&stride_bytes)[2],
+                      const uint32_t (&box)[3], int swizzle_bytes);
 
 // Number of SMs of the current device (cached per device).
 int moe_num_sms();

@@ -13,8 +13,9 @@
 //     three bf16 terms (hi + mid + lo holds its 24 bits) and every 64 deep
 //     block of the product takes three MMAs.  Two terms would lose 2^-17 of a
 //     gradient, which the router keeps in high precision.
-//  3. reduce_kernel -- adds the partial tiles of dC, whose depth T is split
-//     over the CTAs, in a fixed order.
+//  3. The partial tiles of dC, whose depth T is split over the CTAs, are added
+//     in a fixed order, by two spare warps of du's CTAs while those work (or
+//     by reduce_kernel where du is not wanted).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -34,8 +35,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// P = experts per lane; lane l owns experts 32 i + l.
-template <int P>
+// Lane l owns experts 4 l + 128 i .. + 3, i < Q: 16-byte accesses (E % 16 == 0).
+template <int Q>
 __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     const float* __restrict__ dgate, const float* __restrict__ logits,
     const int32_t* __restrict__ idx, const float* __restrict__ gate, int T, int E, int K,
@@ -44,71 +45,92 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRgThreads / 32) + (threadIdx.x >> 5);
   if (t >= T) return;
-  float rest[P], out[P], s[P];
+  float4 z[Q];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
-    out[i] = rest[i] = s[i] = 0.f;
-    if (e < E) {
-      const float z = __ldg(logits + t * E + e);
-      rest[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(z)));
-      s[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-z)));
+  for (int i = 0; i < Q; ++i) {
+    const int e = 128 * i + 4 * lane;
+    z[i] = e < E ? __ldg(reinterpret_cast<const float4*>(logits + t * E + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float g = 0.f, a = 0.f;
+  int mine = -1;
+  if (dgate && lane < K) {
+    g = __ldg(gate + t * K + lane);
+    a = __ldg(dgate + t * K + lane);
+    mine = __ldg(idx + t * K + lane);
+    if (mine < 0 || mine >= E) {
+      set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
+      mine = -1;
+      g = 0.f;
+    }
+  }
+  // s and 1 - s from one exponential: e^-|z| / (1 + e^-|z|) and 1 / (1 + e^-|z|)
+  float s[4 * Q], rest[4 * Q], out[4 * Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const float v[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+    const bool in = 128 * i + 4 * lane < E;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float em = expf(-fabsf(v[j]));
+      const float big = __frcp_rn(__fadd_rn(1.0f, em)), small = __fmul_rn(em, big);
+      s[4 * i + j] = in ? (v[j] >= 0.f ? big : small) : 0.f;
+      rest[4 * i + j] = v[j] >= 0.f ? small : big;
+      out[4 * i + j] = 0.f;
     }
   }
   if (f) {
     const int64_t q = t / seq_len;
     const float c0 = __fmul_rn(alpha, dloss ? __ldg(dloss + q) : 1.0f) / static_cast<float>(seq_len);
-    float c[P], sum = 0.f, mean = 0.f;
+    float c[4 * Q], sum = 0.f, mean = 0.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = 32 * i + lane;
-      c[i] = e < E ? __fmul_rn(c0, __ldg(f + q * E + e)) : 0.f;
-      sum = __fadd_rn(sum, s[i]);
-      mean = fmaf(s[i], c[i], mean);
-    }
-    sum = warp_sum(sum);
-    mean = __fdiv_rn(warp_sum(mean), sum);
+    for (int i = 0; i < Q; ++i) {
+      const int e = 128 * i + 4 * lane;
+      const float4 w = e < E ? __ldg(reinterpret_cast<const float4*>(f + q * E + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      c[4 * i] = __fmul_rn(c0, w.x);
+      c[4 * i + 1] = __fmul_rn(c0, w.y);
+      c[4 * i + 2] = __fmul_rn(c0, w.z);
+      c[4 * i + 3] = __fmul_rn(c0, w.w);
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      out[i] = __fmul_rn(__fmul_rn(__fdiv_rn(s[i], sum), rest[i]), __fsub_rn(c[i], mean));
-  }
-  if (dgate) {
-    float g = 0.f, a = 0.f;
-    int e = -1;
-    if (lane < K) {
-      g = __ldg(gate + t * K + lane);
-      a = __ldg(dgate + t * K + lane);
-      e = __ldg(idx + t * K + lane);
-      if (e < 0 || e >= E) {
-        set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
-        e = -1;
-        g = 0.f;
+      for (int j = 4 * i; j < 4 * i + 4; ++j) {
+        sum = __fadd_rn(sum, s[j]);
+        mean = fmaf(s[j], c[j], mean);
       }
     }
+    const float inv = __fdiv_rn(1.0f, warp_sum(sum));
+    mean = __fmul_rn(warp_sum(mean), inv);
+#pragma unroll
+    for (int j = 0; j < 4 * Q; ++j)
+      out[j] = __fmul_rn(__fmul_rn(__fmul_rn(s[j], inv), rest[j]), __fsub_rn(c[j], mean));
+  }
+  if (dgate) {
     const float mean = warp_sum(__fmul_rn(g, a));
     const float part = __fmul_rn(g, __fsub_rn(a, mean));
     for (int k = 0; k < K; ++k) {
-      const int ek = __shfl_sync(0xffffffffu, e, k);
+      const int ek = __shfl_sync(0xffffffffu, mine, k) - 4 * lane;
       const float pk = __shfl_sync(0xffffffffu, part, k);
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (ek == 32 * i + lane) out[i] = fmaf(pk, rest[i], out[i]);
+      for (int j = 0; j < 4 * Q; ++j)
+        if (ek == 128 * (j / 4) + j % 4) out[j] = fmaf(pk, rest[j], out[j]);
     }
   }
   const int64_t plane = static_cast<int64_t>(T) * E;
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
+  for (int i = 0; i < Q; ++i) {
+    const int e = 128 * i + 4 * lane;
     if (e >= E) continue;
-    if (dz) dz[t * E + e] = out[i];
+    float r[4] = {out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
+    if (dz) *reinterpret_cast<float4*>(dz + t * E + e) = make_float4(r[0], r[1], r[2], r[3]);
     if (terms) {
       // hi + mid + lo = out: each difference is exact
-      float r = out[i];
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(r);
-        terms[j * plane + t * E + e] = __bfloat16_as_ushort(h);
-        r = __fsub_rn(r, __bfloat162float(h));
+      for (int m = 0; m < 3; ++m) {
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(r[0], r[1]), h1 = __floats2bfloat162_rn(r[2], r[3]);
+        *reinterpret_cast<uint2*>(terms + m * plane + t * E + e) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        r[0] = __fsub_rn(r[0], __low2float(h0));
+        r[1] = __fsub_rn(r[1], __high2float(h0));
+        r[2] = __fsub_rn(r[2], __low2float(h1));
+        r[3] = __fsub_rn(r[3], __high2float(h1));
       }
     }
   }
@@ -119,56 +141,92 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 // B bf16, N contiguous (the tensor core reads it as an MN-major operand).
 //   du: A = dz as stored (M = tokens, depth = experts), B = the centroids
 //   dC: A = dz transposed, also MN-major (M = experts, depth = tokens), B = u
-// Tiles of 128 x 256 over depth blocks of 64.  One warp issues TMA loads into
-// a two-stage ring (80 KB a stage: 3 x 16 KB of A, 32 KB of B), one thread
-// issues the MMAs, eight warps add finished accumulators in registers: the
-// two TMEM accumulators alternate every 128 deep, so that a tensor-core sum,
-// whose additions may truncate, stays 24 steps long and the rest is rounded
-// fp32 additions.  The depth blocks of all tiles form one line that is cut
-// evenly over the CTAs (for du at tile borders): every SM gets the same work
-// whatever the shape, and dC's few tiles still fill the GPU.
-constexpr int kPrM = 128, kPrN = 256, kPrK = 64;
-constexpr int kPrStages = 2;
-constexpr int kPrChunk = 2;                       // depth blocks per accumulator
+// Tiles of 128 x 256 over depth blocks of 32.  One thread issues the TMA
+// loads of a ring of 40 KB stages (24 KB of A, all three terms in one box or
+// two; 16 KB of B), one thread issues the MMAs, eight warps add finished
+// accumulators in registers: the two TMEM accumulators alternate every 128
+// deep, so that a tensor-core sum, whose additions may truncate, stays 24
+// steps long and the rest is rounded fp32 additions.  The depth blocks of all
+// tiles form one line that is cut evenly over the CTAs (for du at tile
+// borders): every SM gets the same work whatever the shape, and dC's few
+// tiles still fill the GPU.
+// du is bound by reading the base and writing du in fp32 (HBM), dC by the
+// tensor cores.  Issuing a TMA load takes its thread about 70 cycles: ten a
+// stage held both back, hence the boxes of three terms.  Each epilogue warp
+// has 32 x 32 patches of its own in shared memory, which TMA fills with the
+// base ahead of time and empties into the result.
+constexpr int kPrM = 128, kPrN = 256, kPrK = 32;
+constexpr int kPrChunk = 4;                       // depth blocks per accumulator
 constexpr int kPrTerm = kPrM * kPrK * 2;          // bytes of one term's A block
+constexpr int kPrSlab = 64 * kPrK * 2;            // 64 columns of an MN-major operand
 constexpr int kPrB = kPrK * kPrN * 2;
 constexpr int kPrStage = 3 * kPrTerm + kPrB;
 constexpr int kPrEpiWarps = 8;
-constexpr int kPrThreads = 128 + 32 * kPrEpiWarps;  // TMA, MMA and two idle warps; the epilogue
-// launched with 168 registers a thread; 128 x 56 + 256 x 224 = 384 x 168
-constexpr int kPrRegsCtl = 56, kPrRegsEpi = 224;
-constexpr int kPrPatch = 32 * 32 * 4;             // a warp's 32 x 32 transpose patch
-constexpr int kPrSmem = 1024 + kPrStages * kPrStage + kPrEpiWarps * kPrPatch + 256;
+constexpr int kPrThreads = 128 + 32 * kPrEpiWarps;  // TMA, MMA and two spare warps; the epilogue
+// launched with 168 registers a thread; 128 x 72 + 256 x 216 = 384 x 168
+constexpr int kPrRegsCtl = 72, kPrRegsEpi = 216;
+constexpr int kPrPatch = 32 * 32 * 4;
 constexpr uint32_t kPrTmemCols = 2 * kPrN;
+// du keeps three patches a warp (two loads of the base in flight while one is
+// used) and a ring of three stages, dC two patches and four stages.
+template <bool A_MN>
+constexpr int kPrStages = A_MN ? 4 : 3;
+template <bool A_MN>
+constexpr int kPrPatches = A_MN ? 2 : 3;
+template <bool A_MN>
+constexpr int kPrSmem = 1024 + kPrStages<A_MN> * kPrStage + kPrPatches<A_MN> * kPrEpiWarps * kPrPatch + 512;
+
+// Depth blocks up to which dC's tiles stay whole (T <= 512).
+constexpr int kPrShort = 16;
+
+// The parts of dC's tiles: CTA c worked on depth blocks [c * per, (c + 1) *
+// per) of the line; its part of its first tile is slot 2 c, of its last 2 c + 1.
+struct Parts {
+  const float* part;
+  float* out;
+  int tiles, KB, per, mt, M, N;
+};
 
 struct ProductArgs {
-  int M, N, KB;        // KB: depth blocks of a tile
-  int mt;              // m tiles (the faster tile index)
-  int64_t units;       // depth blocks of all tiles
-  int whole;           // cut at tile borders only
-  const float* base;   // may be out
-  float* out;
-  float* part;         // partial tiles [2 * CTAs][128][256]
+  int M, N, KB;  // KB: depth blocks of a tile
+  int mt;        // m tiles (the faster tile index)
+  int units;     // depth blocks of all tiles
+  int per;       // depth blocks of a CTA; 0: whole tiles, evenly
+  int has_base;
+  Parts parts;   // du: dC's parts to add (tiles 0: none)
   int32_t* dev_err;
 };
 
-// First depth block of CTA c of G.
-__host__ __device__ inline int64_t cut(int64_t units, int KB, int whole, int c, int G) {
-  return whole ? units / KB * c / G * KB : units * c / G;
-}
-
 // MN-major operand with the 128-byte swizzle: TMA boxes of 64 (contiguous)
-// x 64 (depth) elements are 8 KB slabs of 128-byte rows.  8 depth rows are a
+// x 32 (depth) elements are 4 KB slabs of 128-byte rows.  8 depth rows are a
 // 1024-byte atom (stride byte offset), the next 64 elements are the next slab
 // (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr) {
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint32_t slab_stride) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(slab_stride >> 4) << 16;
   d |= static_cast<uint64_t>(1024u >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
+}
+
+// TMA store of a patch, and the wait for all but the last N stores to have
+// read (or, Done, written) theirs.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t c0,
+                                             int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 struct Segment {
@@ -178,39 +236,85 @@ struct Segment {
 };
 
 // The next stretch of one tile in [pos, end).
-__device__ __forceinline__ Segment next_segment(const ProductArgs& a, int64_t start, int64_t pos,
-                                                int64_t end) {
+__device__ __forceinline__ Segment next_segment(const ProductArgs& a, int start, int pos, int end) {
   Segment s;
-  const int64_t tile = pos / a.KB;
-  s.k0 = static_cast<int>(pos - tile * a.KB);
-  s.k1 = static_cast<int>(min(static_cast<int64_t>(a.KB), s.k0 + (end - pos)));
-  s.m0 = static_cast<int>(tile % a.mt) * kPrM;
-  s.n0 = static_cast<int>(tile / a.mt) * kPrN;
+  const int tile = pos / a.KB;
+  s.k0 = pos - tile * a.KB;
+  s.k1 = min(a.KB, s.k0 + (end - pos));
+  s.m0 = tile % a.mt * kPrM;
+  s.n0 = tile / a.mt * kPrN;
   s.whole = s.k0 == 0 && s.k1 == a.KB;
   s.first = pos == start;
   return s;
 }
 
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x = __fadd_rn(a.x, b.x);
+  a.y = __fadd_rn(a.y, b.y);
+  a.z = __fadd_rn(a.z, b.z);
+  a.w = __fadd_rn(a.w, b.w);
+}
+
+// Adds the parts of every tile that more than one CTA worked on, CTA by CTA;
+// 64 threads take four rows of a tile at a time.
+__device__ __forceinline__ void add_parts(const Parts& a, int worker, int workers, int thread) {
+  constexpr int kRows = 4;
+  for (int g = worker; g < a.tiles * (kPrM / kRows); g += workers) {
+    const int tile = g / (kPrM / kRows), r0 = g % (kPrM / kRows) * kRows;
+    const int c0 = tile * a.KB / a.per, c1 = ((tile + 1) * a.KB - 1) / a.per;
+    if (c0 == c1) continue;
+    const int m = tile % a.mt * kPrM + r0, n = tile / a.mt * kPrN + 4 * thread;
+    if (m >= a.M || n >= a.N) continue;  // M is a multiple of four rows
+    auto at = [&](int c) {
+      const int slot = 2 * c + (c * a.per / a.KB == tile ? 0 : 1);
+      return reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(slot) * (kPrM * kPrN) + r0 * kPrN) + thread;
+    };
+    float4 sum[kRows], more[kRows];
+    const float4 *p = at(c0), *q = at(c0 + 1);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) sum[r] = __ldg(p + r * (kPrN / 4));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) more[r] = __ldg(q + r * (kPrN / 4));
+    for (int c = c0 + 1;;) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) add4(sum[r], more[r]);
+      if (++c > c1) break;
+      q = at(c);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) more[r] = __ldg(q + r * (kPrN / 4));
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      *reinterpret_cast<float4*>(a.out + static_cast<int64_t>(m + r) * a.N + n) = sum[r];
+  }
+}
+
+__global__ void __launch_bounds__(64) reduce_kernel(const Parts parts) {
+  add_parts(parts, blockIdx.x, gridDim.x, threadIdx.x);
+}
+
 template <bool A_MN>
 __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
-    const __grid_constant__ CUtensorMap tmHi, const __grid_constant__ CUtensorMap tmMid,
-    const __grid_constant__ CUtensorMap tmLo, const __grid_constant__ CUtensorMap tmB,
-    const ProductArgs args) {
+    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmOut,
+    const __grid_constant__ CUtensorMap tmPart, const ProductArgs args) {
+  constexpr int kStages = kPrStages<A_MN>, kPatches = kPrPatches<A_MN>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* patches = ring + kPrStages * kPrStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(patches + kPrEpiWarps * kPrPatch);
-  uint64_t* empty = full + kPrStages;
-  uint64_t* acc_full = empty + kPrStages;
+  uint8_t* patches = ring + kStages * kPrStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(patches + kPatches * kPrEpiWarps * kPrPatch);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* base_full = done + 1;  // [epilogue warp][patch]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_full + kPatches * kPrEpiWarps);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPrStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -218,13 +322,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       mbar_init(&acc_full[p], 1);
       mbar_init(&acc_empty[p], kPrEpiWarps);
     }
+    for (int p = 0; p < kPatches * kPrEpiWarps; ++p) mbar_init(&base_full[p], 1);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&tmHi);
-    prefetch_tmap(&tmMid);
-    prefetch_tmap(&tmLo);
+    prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
+    prefetch_tmap(&tmOut);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kPrTmemCols);
@@ -235,45 +339,48 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile int* abort_v = abort_flag;
-  const int64_t start = cut(args.units, args.KB, args.whole, blockIdx.x, gridDim.x);
-  const int64_t end = cut(args.units, args.KB, args.whole, blockIdx.x + 1, gridDim.x);
+  int start, end;
+  if (args.per) {
+    start = min(args.units, static_cast<int>(blockIdx.x) * args.per);
+    end = min(args.units, start + args.per);
+  } else {
+    const int64_t tiles = args.units / args.KB;
+    start = static_cast<int>(tiles * blockIdx.x / gridDim.x) * args.KB;
+    end = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) * args.KB;
+  }
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsCtl));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsCtl));
     if (warp == 0 && lane == 0) {
       // --------------------------------------------------------- TMA producer
-      const CUtensorMap* tmA[3] = {&tmLo, &tmMid, &tmHi};
       int it = 0;
       bool live = true;
-      for (int64_t pos = start; pos < end && live;) {
+      for (int pos = start; pos < end && live;) {
         const Segment g = next_segment(args, start, pos, end);
         pos += g.k1 - g.k0;
         for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
-          const int s = it % kPrStages;
-          if (!mbar_wait(&empty[s], ((it / kPrStages) & 1) ^ 1, abort_v, args.dev_err)) {
+          const int s = it % kStages;
+          if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, abort_v, args.dev_err)) {
             live = false;
             break;
           }
           uint8_t* sA = ring + s * kPrStage;
           uint8_t* sB = sA + 3 * kPrTerm;
           mbar_arrive_expect_tx(&full[s], kPrStage);
-#pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            if (A_MN) {
-              tma_load_2d(sA + j * kPrTerm, tmA[j], &full[s], g.m0, kb * kPrK);
-              tma_load_2d(sA + j * kPrTerm + 8192, tmA[j], &full[s], g.m0 + 64, kb * kPrK);
-            } else {
-              tma_load_2d(sA + j * kPrTerm, tmA[j], &full[s], kb * kPrK, g.m0);
-            }
+          if (A_MN) {  // [64 experts][term][depth][64]
+            tma_load_3d(sA, &tmA, &full[s], g.m0, kb * kPrK, 0);
+            tma_load_3d(sA + 3 * kPrSlab, &tmA, &full[s], g.m0 + 64, kb * kPrK, 0);
+          } else {     // [term][row][depth]
+            tma_load_3d(sA, &tmA, &full[s], kb * kPrK, g.m0, 0);
           }
 #pragma unroll
           for (int j = 0; j < kPrN / 64; ++j)
-            tma_load_2d(sB + j * 8192, &tmB, &full[s], g.n0 + 64 * j, kb * kPrK);
+            tma_load_2d(sB + j * kPrSlab, &tmB, &full[s], g.n0 + 64 * j, kb * kPrK);
         }
       }
       // every issued copy lands before the CTA can exit
-      for (int i = it > kPrStages ? it - kPrStages : 0; i < it; ++i)
-        mbar_wait(&full[i % kPrStages], (i / kPrStages) & 1, nullptr, args.dev_err);
+      for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
+        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, args.dev_err);
     } else if (warp == 1 && lane == 0) {
       // ----------------------------------------------------------- MMA issuer
       const uint32_t idesc = instr_desc(kFmtBF16, kFmtBF16, kPrM, kPrN) | (A_MN ? 1u << 15 : 0u) | (1u << 16);
@@ -281,7 +388,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       constexpr uint64_t kStepB = 2048 >> 4;
       int it = 0, ch = 0;
       bool live = true;
-      for (int64_t pos = start; pos < end && live;) {
+      for (int pos = start; pos < end && live;) {
         const Segment g = next_segment(args, start, pos, end);
         pos += g.k1 - g.k0;
         for (int kc = g.k0; kc < g.k1 && live; kc += kPrChunk, ++ch) {
@@ -294,20 +401,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
           const uint32_t acc = tmem + static_cast<uint32_t>(p * kPrN);
           const int kend = min(kc + kPrChunk, g.k1);
           for (int kb = kc; kb < kend; ++kb, ++it) {
-            const int s = it % kPrStages;
-            if (!mbar_wait(&full[s], (it / kPrStages) & 1, abort_v, args.dev_err)) {
+            const int s = it % kStages;
+            if (!mbar_wait(&full[s], (it / kStages) & 1, abort_v, args.dev_err)) {
               live = false;
               break;
             }
             tc_fence_after();
             const uint32_t sA = smem_u32(ring + s * kPrStage);
-            const uint64_t bd = smem_desc_mn_sw128(sA + 3 * kPrTerm);
+            const uint64_t bd = smem_desc_mn_sw128(sA + 3 * kPrTerm, kPrSlab);
 #pragma unroll
             for (int k = 0; k < kPrK / 16; ++k)
 #pragma unroll
-              for (int j = 0; j < 3; ++j) {
-                const uint64_t ad = A_MN ? smem_desc_mn_sw128(sA + j * kPrTerm) : smem_desc_sw128(sA + j * kPrTerm);
-                mma_f16(acc, ad + k * kStepA, bd + k * kStepB, idesc, (kb > kc || k > 0 || j > 0) ? 1u : 0u);
+              for (int j = 2; j >= 0; --j) {  // the smallest term first
+                const uint64_t ad = A_MN ? smem_desc_mn_sw128(sA + j * kPrSlab, 3 * kPrSlab)
+                                         : smem_desc_sw64(sA + j * kPrTerm);
+                mma_f16(acc, ad + k * kStepA, bd + k * kStepB, idesc, (kb > kc || k > 0 || j < 2) ? 1u : 0u);
               }
             mma_commit(&empty[s]);
           }
@@ -316,19 +424,43 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       }
       mma_commit(done);
       mbar_wait(done, 0, nullptr, args.dev_err);
+    } else if (!A_MN && warp >= 2 && args.parts.tiles) {
+      add_parts(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsEpi));
+    // --------------------------------------------------------------- epilogue
     // a warp reads the TMEM lanes of its quarter (warp % 4): 32 rows, 128 columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsEpi));
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-    float4* patch = reinterpret_cast<float4*>(patches + (warp - 4) * kPrPatch);
-    const int pr = lane >> 3, pc = lane & 7;  // row group and 16-byte column when reading a patch
+    uint8_t* patch = patches + (warp - 4) * kPatches * kPrPatch;
+    uint64_t* landed = base_full + kPatches * (warp - 4);
+    // the base's patches, loaded ahead of their use: tile and patch of the
+    // next load, loads issued (all of lane 0), patches used
+    const int t1 = end / args.KB;
+    int lt = start / args.KB, lb = 0, loads = 0, used = 0;
+    auto load_next = [&]() {
+      while (lt < t1 && (lt / args.mt * kPrN + half * 128 >= args.N || lt % args.mt * kPrM + quarter * 32 >= args.M)) ++lt;
+      if (lt >= t1) return;
+      const int b = loads % kPatches;
+      mbar_arrive_expect_tx(&landed[b], kPrPatch);
+      tma_load_2d(patch + b * kPrPatch, &tmBase, &landed[b], lt / args.mt * kPrN + half * 128 + 32 * lb,
+                  lt % args.mt * kPrM + quarter * 32);
+      ++loads;
+      if (++lb == 4) {
+        lb = 0;
+        ++lt;
+      }
+    };
+    const bool has_base = !A_MN && args.has_base;
+    if (has_base && lane == 0) {
+#pragma unroll
+      for (int i = 0; i < kPatches; ++i) load_next();
+    }
     int ch = 0;
     bool ok = true;
-    for (int64_t pos = start; pos < end && ok;) {
+    for (int pos = start; pos < end && ok;) {
       const Segment g = next_segment(args, start, pos, end);
       pos += g.k1 - g.k0;
       float acc[128];
@@ -340,12 +472,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          float v[16];
-          tmem_ld16(tq + p * kPrN + c, v);
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          tmem_ld32(tq + p * kPrN + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = __fadd_rn(acc[c + i], v[i]);
+          for (int i = 0; i < 32; ++i) acc[c + i] = __fadd_rn(acc[c + i], v[i]);
         }
         tc_fence_before();
         __syncwarp();
@@ -354,118 +486,87 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       if (!ok) break;
       // whole tiles go to the result, a part of a tile to the CTA's slot of
       // its first or its last tile
-      const bool direct = g.whole;
-      const int row0 = direct ? g.m0 + quarter * 32 : quarter * 32;
+      const bool direct = !A_MN || g.whole;
+      if (direct && (g.n0 + half * 128 >= args.N || g.m0 + quarter * 32 >= args.M)) continue;
+      const CUtensorMap* dst = direct ? &tmOut : &tmPart;
+      const int row0 = direct ? g.m0 + quarter * 32 : (2 * static_cast<int>(blockIdx.x) + (g.first ? 0 : 1)) * kPrM + quarter * 32;
       const int col0 = direct ? g.n0 + half * 128 : half * 128;
-      const int rows = direct ? min(32, args.M - row0) : 32;
-      const int64_t ld = direct ? args.N : kPrN;
-      float* dst = direct ? args.out
-                          : args.part + (2 * static_cast<int64_t>(blockIdx.x) + (g.first ? 0 : 1)) * (kPrM * kPrN);
-      const float* base = direct ? args.base : nullptr;
-      if (direct && col0 >= args.N) continue;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        // lane = row into the patch (chunks swizzled by the row), then rows of 128 bytes out
+      for (int b = 0; b < 4; ++b, ++used) {
+        uint8_t* buf = patch + used % kPatches * kPrPatch;
+        if (has_base) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&landed[used % kPatches], (used / kPatches) & 1, abort_v, args.dev_err));
+          if (!ok) break;
+        } else {
+          if (lane == 0) tma_store_wait_read<kPatches - 1>();  // this patch's last store has read it
+          __syncwarp();
+        }
+        // lane = row of 128 bytes, 16-byte pieces swizzled as TMA does
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          patch[lane * 8 + (c ^ (lane & 7))] =
-              make_float4(acc[32 * b + 4 * c], acc[32 * b + 4 * c + 1], acc[32 * b + 4 * c + 2], acc[32 * b + 4 * c + 3]);
+        for (int c = 0; c < 8; ++c) {
+          float4* at = reinterpret_cast<float4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4));
+          float4 v = make_float4(acc[32 * b + 4 * c], acc[32 * b + 4 * c + 1], acc[32 * b + 4 * c + 2], acc[32 * b + 4 * c + 3]);
+          if (has_base) add4(v, *at);
+          *at = v;
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-        float4 add[8];
-        if (base) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + pr;
-            if (r < rows)
-              add[i] = *reinterpret_cast<const float4*>(base + (row0 + r) * ld + col0 + 32 * b + 4 * pc);
+        if (lane == 0) {
+          tma_store_2d(dst, buf, col0 + 32 * b, row0);
+          if (has_base && used > 0) {  // the patch before this one has been stored: load ahead into it
+            tma_store_wait_read<1>();
+            load_next();
           }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + pr;
-          float4 v = patch[r * 8 + (pc ^ (r & 7))];
-          if (r < rows) {
-            if (base) {
-              v.x = __fadd_rn(v.x, add[i].x);
-              v.y = __fadd_rn(v.y, add[i].y);
-              v.z = __fadd_rn(v.z, add[i].z);
-              v.w = __fadd_rn(v.w, add[i].w);
-            }
-            *reinterpret_cast<float4*>(dst + (row0 + r) * ld + col0 + 32 * b + 4 * pc) = v;
-          }
-        }
-        __syncwarp();
       }
     }
+    // every copy of this warp has landed or left before the CTA can exit
+    if (lane == 0) {
+      for (int i = used; i < loads; ++i) mbar_wait(&landed[i % kPatches], (i / kPatches) & 1, nullptr, args.dev_err);
+      tma_store_wait_done();
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, kPrTmemCols);
 }
 
-// The CTA whose share holds depth block x.
-__host__ __device__ inline int owner(int64_t x, int64_t units, int G) {
-  int c = static_cast<int>((x * G) / units);
-  while (c + 1 < G && units * (c + 1) / G <= x) ++c;
-  while (c > 0 && units * c / G > x) --c;
-  return c;
-}
-
-// Adds the parts of every tile that more than one CTA worked on, CTA by CTA.
-__global__ void __launch_bounds__(256) reduce_kernel(const float* __restrict__ part, int64_t units,
-                                                     int KB, int mt, int G, int M, int N,
-                                                     float* __restrict__ out) {
-  const int tile = blockIdx.x;
-  const int c0 = owner(static_cast<int64_t>(tile) * KB, units, G);
-  const int c1 = owner(static_cast<int64_t>(tile + 1) * KB - 1, units, G);
-  if (c0 == c1) return;
-  const int m0 = tile % mt * kPrM, n0 = tile / mt * kPrN;
-  // 8 rows of 256 columns a block
-  const int v = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = blockIdx.y * 8 + i * 4 + (threadIdx.x >> 6);
-    if (m0 + r >= M || n0 + 4 * v >= N) continue;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const int slot = 2 * c + (units * c / G / KB == tile ? 0 : 1);
-      const float4 p = __ldg(reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot) * (kPrM * kPrN) + r * kPrN) + v);
-      sum.x = __fadd_rn(sum.x, p.x);
-      sum.y = __fadd_rn(sum.y, p.y);
-      sum.z = __fadd_rn(sum.z, p.z);
-      sum.w = __fadd_rn(sum.w, p.w);
-    }
-    *reinterpret_cast<float4*>(out + static_cast<int64_t>(m0 + r) * N + n0 + 4 * v) = sum;
-  }
-}
-
-template <int P>
+template <int Q>
 void launch_dlogits(cudaStream_t st, const float* dgate, const float* logits, const int32_t* idx,
                     const float* gate, int T, int E, int K, const float* f, const float* dloss,
                     int seq_len, float alpha, float* dz, uint16_t* terms, int32_t* dev_err) {
   const int blocks = (T + kRgThreads / 32 - 1) / (kRgThreads / 32);
-  dlogits_kernel<P><<<blocks, kRgThreads, 0, st>>>(dgate, logits, idx, gate, T, E, K, f, dloss,
+  dlogits_kernel<Q><<<blocks, kRgThreads, 0, st>>>(dgate, logits, idx, gate, T, E, K, f, dloss,
                                                    seq_len, alpha, dz, terms, dev_err);
 }
 
 struct Plan {
   size_t terms, parts;  // workspace bytes
-  int64_t du_units, dc_units;
-  int du_kb, du_mt, du_ctas, dc_kb, dc_mt, dc_ctas;
+  int du_units, du_kb, du_mt, du_ctas;
+  int dc_units, dc_kb, dc_mt, dc_per, dc_ctas;
+  bool fits;
 };
 
 Plan make_plan(int T, int d, int E) {
   Plan p;
-  const int sms = moe_num_sms();
+  const int64_t sms = moe_num_sms();
   const int64_t nt = (d + kPrN - 1) / kPrN;
-  p.du_mt = (T + kPrM - 1) / kPrM;
-  p.du_kb = (E + kPrK - 1) / kPrK;
-  p.du_units = p.du_mt * nt * p.du_kb;
-  p.du_ctas = static_cast<int>(std::min<int64_t>(sms, p.du_mt * nt));
-  p.dc_mt = (E + kPrM - 1) / kPrM;
-  p.dc_kb = (T + kPrK - 1) / kPrK;
-  p.dc_units = p.dc_mt * nt * p.dc_kb;
-  p.dc_ctas = static_cast<int>(std::min<int64_t>(sms, p.dc_units));
+  const int64_t tm = (static_cast<int64_t>(T) + kPrM - 1) / kPrM, tk = (static_cast<int64_t>(T) + kPrK - 1) / kPrK;
+  const int64_t em = (E + kPrM - 1) / kPrM, ek = (E + kPrK - 1) / kPrK;
+  const int64_t du = tm * nt * ek, dc = em * nt * tk;
+  p.fits = du < (1ll << 31) && dc < (1ll << 31);
+  p.du_units = static_cast<int>(du);
+  p.du_kb = static_cast<int>(ek);
+  p.du_mt = static_cast<int>(tm);
+  p.du_ctas = static_cast<int>(std::min(sms, tm * nt));
+  p.dc_units = static_cast<int>(dc);
+  p.dc_kb = static_cast<int>(tk);
+  p.dc_mt = static_cast<int>(em);
+  // a short depth is not split: adding the parts would cost more than it saves
+  const int64_t per = (dc + sms - 1) / sms;
+  p.dc_per = static_cast<int>(tk <= kPrShort ? (per + tk - 1) / (tk ? tk : 1) * tk : per);
+  p.dc_ctas = p.dc_per ? static_cast<int>((dc + p.dc_per - 1) / p.dc_per) : 0;
   p.terms = (static_cast<size_t>(T) * E * 2 * 3 + 255) / 256 * 256;
   p.parts = static_cast<size_t>(2) * p.dc_ctas * kPrM * kPrN * sizeof(float);
   return p;
@@ -477,8 +578,8 @@ bool grant_smem() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (dev >= 0 && dev < 64 && done[dev]) return true;
-  if (cudaFuncSetAttribute(product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<true>) != cudaSuccess ||
+      cudaFuncSetAttribute(product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<false>) != cudaSuccess)
     return false;
   if (dev >= 0 && dev < 64) done[dev] = true;
   return true;
@@ -502,6 +603,7 @@ extern "C" moe_status moe_route_backward_workspace_size(int T, int d, int E, siz
   const moe_status s = moe::check_sizes(T, d, E);
   if (s != MOE_OK) return s;
   const moe::Plan p = moe::make_plan(T, d, E);
+  if (!p.fits) return MOE_ERR_UNSUPPORTED;
   *bytes = p.terms + p.parts;
   return MOE_OK;
 }
@@ -531,48 +633,53 @@ extern "C" moe_status moe_route_backward(
       !aligned4(dgate) || !aligned4(topk_idx) || !aligned4(topk_gate) || !aligned4(f) || !aligned4(dloss))
     return MOE_ERR_ALIGN;
   size_t need = 0;
-  moe_route_backward_workspace_size(T, d, E, &need);
+  if (moe_route_backward_workspace_size(T, d, E, &need) != MOE_OK) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < need || !ws) return MOE_ERR_WORKSPACE;
   if (!aligned16(ws)) return MOE_ERR_ALIGN;
   const Plan plan = make_plan(T, d, E);
+  if (!plan.fits) return MOE_ERR_UNSUPPORTED;
   uint16_t* terms = static_cast<uint16_t*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.terms);
   const bool products = du || dcentroids;
   if (products && !grant_smem()) return MOE_ERR_CUDA;
-  const int P = (E + 31) / 32;
-  auto go = P <= 1 ? launch_dlogits<1> : P <= 2 ? launch_dlogits<2> : P <= 4 ? launch_dlogits<4>
-          : P <= 8 ? launch_dlogits<8> : P <= 12 ? launch_dlogits<12> : P <= 16 ? launch_dlogits<16>
-          : launch_dlogits<32>;
+  const int Q = (E + 127) / 128;
+  auto go = Q <= 1 ? launch_dlogits<1> : Q <= 2 ? launch_dlogits<2> : Q <= 3 ? launch_dlogits<3>
+          : Q <= 4 ? launch_dlogits<4> : launch_dlogits<8>;
   go(st, dgate, logits, topk_idx, topk_gate, T, E, K, f, dloss, seq_len, alpha, dlogits,
      products ? terms : nullptr, dev_err);
   MOE_CUDA_CHECK_LAUNCH();
 
-  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const size_t plane = static_cast<size_t>(T) * E;
-  CUtensorMap a[3], b;
-  if (du) {
-    for (int j = 0; j < 3; ++j)
-      if (!moe_make_tmap_2d(&a[j], terms + j * plane, bf16, E, T, static_cast<uint64_t>(E) * 2, kPrK, kPrM))
-        return MOE_ERR_CUDA;
-    if (!moe_make_tmap_2d(&b, centroids, bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK)) return MOE_ERR_CUDA;
-    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 1, du_base, du, nullptr, dev_err};
-    product_kernel<false><<<plan.du_ctas, kPrThreads, kPrSmem, st>>>(a[0], a[1], a[2], b, args);
-    MOE_CUDA_CHECK_LAUNCH();
-  }
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const uint64_t rd = static_cast<uint64_t>(d) * 4, rz = static_cast<uint64_t>(E) * 2;
+  const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), 3}, stride[2] = {rz, rz * T};
+  const uint32_t box_mn[3] = {64, kPrK, 3}, box_k[3] = {kPrK, kPrM, 3};
+  CUtensorMap a, b, in, out, part;
+  Parts left{};  // dC's parts that are still to be added
   if (dcentroids) {
-    for (int j = 0; j < 3; ++j)
-      if (!moe_make_tmap_2d(&a[j], terms + j * plane, bf16, E, T, static_cast<uint64_t>(E) * 2, 64, kPrK))
-        return MOE_ERR_CUDA;
-    if (!moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK)) return MOE_ERR_CUDA;
-    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, 0, nullptr, dcentroids, parts, dev_err};
-    product_kernel<true><<<plan.dc_ctas, kPrThreads, kPrSmem, st>>>(a[0], a[1], a[2], b, args);
+    if (!moe_make_tmap_3d(&a, terms, bf16, extent, stride, box_mn, 128) ||
+        !moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
+        !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
+        !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32))
+      return MOE_ERR_CUDA;
+    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, Parts{}, dev_err};
+    product_kernel<true><<<plan.dc_ctas, kPrThreads, kPrSmem<true>, st>>>(a, b, out, out, part, args);
     MOE_CUDA_CHECK_LAUNCH();
-    const int64_t tiles = plan.dc_units / plan.dc_kb;
-    if (plan.dc_kb > 1) {  // a tile of one depth block has one owner
-      reduce_kernel<<<dim3(static_cast<unsigned>(tiles), kPrM / 8), 256, 0, st>>>(
-          parts, plan.dc_units, plan.dc_kb, plan.dc_mt, plan.dc_ctas, E, d, dcentroids);
-      MOE_CUDA_CHECK_LAUNCH();
-    }
+    if (plan.dc_per % plan.dc_kb != 0)  // else every CTA's tiles are whole
+      left = Parts{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
+  }
+  if (du) {
+    if (!moe_make_tmap_3d(&a, terms, bf16, extent, stride, box_k, 64) ||
+        !moe_make_tmap_2d(&b, centroids, bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK) ||
+        !moe_make_tmap_2d(&in, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
+        !moe_make_tmap_2d(&out, du, fp32, d, T, rd, 32, 32))
+      return MOE_ERR_CUDA;
+    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, left, dev_err};
+    product_kernel<false><<<plan.du_ctas, kPrThreads, kPrSmem<false>, st>>>(a, b, in, out, out, args);
+    MOE_CUDA_CHECK_LAUNCH();
+  } else if (left.tiles) {
+    const int groups = left.tiles * (kPrM / 4);
+    reduce_kernel<<<std::min(groups, 8 * moe_num_sms()), 64, 0, st>>>(left);
+    MOE_CUDA_CHECK_LAUNCH();
   }
   return MOE_OK;
 }

@@ -71,6 +71,8 @@ def _check(c, n_seq, out, alpha=1e-2):
     bound = (3 * E + 8) * 2.0 ** -23 * (dz.abs() @ c["cent"].double().abs()) + 2.0 ** -23 * (ref.abs() + c["base"].double().abs())
     err = (du.double() - ref).abs()
     assert bool((err <= bound).all()), float((err - bound).max())
+    if dc is None:
+        return
     ref = dz.T @ c["u"].double()
     bound = (3 * T + 8) * 2.0 ** -23 * (dz.abs().T @ c["u"].double().abs()) + 2.0 ** -23 * ref.abs()
     err = (dc.double() - ref).abs()
@@ -263,9 +265,12 @@ def test_layer_with_router_gradient(cuda_dev):
     c = dict(z=layer.logits, gate=layer.gate, dgate=r1["dgate"], idx=layer.idx, f=layer.balance.f, dloss=dbal,
              u=u, cent=cent, base=r0["du"])
     _check(c, cfg.T // S, (r1["dlogits"], r1["du"], r1["dcentroids"]), alpha=1e-4)
-    # no weight gradients wanted: the same du
+    # no weight gradients wanted: du by the same formula (the gates' sums may
+    # run in another order without dy)
     r2 = layer.backward(dout, weight_grads=False, dbalance=dbal)
-    assert torch.equal(r2["du"], r1["du"]) and "dcentroids" not in r2
+    assert "dcentroids" not in r2
+    assert bool(((r2["dgate"].double() - prod.sum(2)).abs() <= bound).all())
+    _check(dict(c, dgate=r2["dgate"]), cfg.T // S, (r2["dlogits"], r2["du"], None), alpha=1e-4)
     with pytest.raises(_abi.MoEError):
         plain.backward(dout, dbalance=dbal)
 
