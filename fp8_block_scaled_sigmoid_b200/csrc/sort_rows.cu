@@ -298,12 +298,12 @@ struct Shape {
   size_t smem;
 };
 
-// Four warps a token where the tokens alone fill the GPU (32 warps an SM),
-// more where they are few, up to 16; several tokens a CTA where a token has
-// fewer pieces.  16384 x 6 rows of 7168 bf16: 475 us with 4 warps, 597 with 8;
-// 256 x 8 of 7168 fp32: 34 us with 4, 30 with 8.
+// Four warps a token where the tokens alone give an SM 64, more where they are
+// few, up to 16; several tokens a CTA where a token has fewer pieces.  16384 x
+// 6 rows of 7168 bf16: 474 us with 4 warps, 597 with 8; 1600 x 8: 73 us with
+// 4, 66 with 5; 256 x 8: 14 us with 4, 9.5 with 14.
 Shape dot_shape(int T, int K, int items) {
-  const int64_t want = (static_cast<int64_t>(moe_num_sms()) * 32 + T - 1) / T;
+  const int64_t want = (static_cast<int64_t>(moe_num_sms()) * 64 + T - 1) / T;
   const int most = static_cast<int>(want < 4 ? 4 : (want > kSrDotWarps ? kSrDotWarps : want));
   const int steps = (items + most - 1) / most;
   const int warps = (items + steps - 1) / steps;
