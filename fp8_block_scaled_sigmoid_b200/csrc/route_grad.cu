@@ -35,6 +35,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The three kernels of a call are launched to overlap: the next one's CTAs come
+// in (and set up their barriers and TMEM) as this one's leave, and wait for its
+// results where they need them.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Lane l owns experts 4 l + 128 i .. + 3, i < Q: 16-byte accesses (E % 16 == 0).
 template <int Q>
 __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
@@ -44,6 +50,7 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     float* __restrict__ dz, uint16_t* __restrict__ terms, int32_t* dev_err) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRgThreads / 32) + (threadIdx.x >> 5);
+  launch_dependents();
   if (t >= T) return;
   float4 z[Q];
 #pragma unroll
@@ -193,6 +200,7 @@ struct ProductArgs {
   int units;     // depth blocks of all tiles
   int per;       // depth blocks of a CTA; 0: whole tiles, evenly
   int has_base;
+  int after_dc;  // du launched behind dC
   Parts parts;   // du: dC's parts to add (tiles 0: none)
   int32_t* dev_err;
 };
@@ -339,6 +347,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile int* abort_v = abort_flag;
+  // dC, and du without dC before it, need the terms that their predecessor
+  // writes.  du after dC finds them complete, since dC lets it start only once
+  // it has them itself: only dC's parts have to be waited for.
+  if (!args.after_dc) wait_predecessor();
+  if (A_MN) launch_dependents();
   int start, end;
   if (args.per) {
     start = min(args.units, static_cast<int>(blockIdx.x) * args.per);
@@ -424,8 +437,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       }
       mma_commit(done);
       mbar_wait(done, 0, nullptr, args.dev_err);
-    } else if (!A_MN && warp >= 2 && args.parts.tiles) {
-      add_parts(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
+    } else if (!A_MN && warp >= 2) {
+      if (args.after_dc) wait_predecessor();
+      if (args.parts.tiles) add_parts(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
     }
     __syncwarp();
   } else {
@@ -585,6 +599,22 @@ bool grant_smem() {
   return true;
 }
 
+// Launches a kernel that may start before the one ahead of it has ended.
+template <typename... P, typename... A>
+bool launch_behind(void (*kern)(P...), int grid, int block, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -661,9 +691,9 @@ extern "C" moe_status moe_route_backward(
         !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
         !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, Parts{}, dev_err};
-    product_kernel<true><<<plan.dc_ctas, kPrThreads, kPrSmem<true>, st>>>(a, b, out, out, part, args);
-    MOE_CUDA_CHECK_LAUNCH();
+    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, Parts{}, dev_err};
+    if (!launch_behind(product_kernel<true>, plan.dc_ctas, kPrThreads, kPrSmem<true>, st, a, b, out, out, part, args))
+      return MOE_ERR_CUDA;
     if (plan.dc_per % plan.dc_kb != 0)  // else every CTA's tiles are whole
       left = Parts{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
   }
@@ -673,9 +703,9 @@ extern "C" moe_status moe_route_backward(
         !moe_make_tmap_2d(&in, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
         !moe_make_tmap_2d(&out, du, fp32, d, T, rd, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, left, dev_err};
-    product_kernel<false><<<plan.du_ctas, kPrThreads, kPrSmem<false>, st>>>(a, b, in, out, out, args);
-    MOE_CUDA_CHECK_LAUNCH();
+    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, dcentroids ? 1 : 0, left, dev_err};
+    if (!launch_behind(product_kernel<false>, plan.du_ctas, kPrThreads, kPrSmem<false>, st, a, b, in, out, out, args))
+      return MOE_ERR_CUDA;
   } else if (left.tiles) {
     const int groups = left.tiles * (kPrM / 4);
     reduce_kernel<<<std::min(groups, 8 * moe_num_sms()), 64, 0, st>>>(left);
