@@ -26,7 +26,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRgThreads = 256;
+constexpr int kRgThreads = 128;
 constexpr int kRgMaxK = 32;
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     const int32_t* __restrict__ idx, const float* __restrict__ gate, int T, int E, int K,
     const float* __restrict__ f, const float* __restrict__ dloss, int seq_len, float alpha,
     float* __restrict__ dz, uint16_t* __restrict__ terms, int32_t* dev_err) {
+  __shared__ float gate_sm[kRgThreads / 32 * 128 * Q];
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRgThreads / 32) + (threadIdx.x >> 5);
   launch_dependents();
@@ -112,12 +113,28 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
   if (dgate) {
     const float mean = warp_sum(__fmul_rn(g, a));
     const float part = __fmul_rn(g, __fsub_rn(a, mean));
-    for (int k = 0; k < K; ++k) {
-      const int ek = __shfl_sync(0xffffffffu, mine, k) - 4 * lane;
-      const float pk = __shfl_sync(0xffffffffu, part, k);
+    // to their experts through shared memory; an index given twice adds in k order
+    float* at = gate_sm + (threadIdx.x >> 5) * 128 * Q;
 #pragma unroll
-      for (int j = 0; j < 4 * Q; ++j)
-        if (ek == 128 * (j / 4) + j % 4) out[j] = fmaf(pk, rest[j], out[j]);
+    for (int i = 0; i < Q; ++i) *reinterpret_cast<float4*>(at + 128 * i + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncwarp();
+    const uint32_t same = __match_any_sync(0xffffffffu, mine < 0 ? -1 - lane : mine);
+    if (__all_sync(0xffffffffu, (same & (same - 1)) == 0)) {
+      if (mine >= 0) at[mine] = part;
+      __syncwarp();
+    } else {
+      for (int k = 0; k < K; ++k) {
+        if (lane == k && mine >= 0) at[mine] += part;
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(at + 128 * i + 4 * lane);
+      out[4 * i] = fmaf(v.x, rest[4 * i], out[4 * i]);
+      out[4 * i + 1] = fmaf(v.y, rest[4 * i + 1], out[4 * i + 1]);
+      out[4 * i + 2] = fmaf(v.z, rest[4 * i + 2], out[4 * i + 2]);
+      out[4 * i + 3] = fmaf(v.w, rest[4 * i + 3], out[4 * i + 3]);
     }
   }
   const int64_t plane = static_cast<int64_t>(T) * E;
