@@ -646,18 +646,20 @@ def grouped_gemm_fp8_wgrad(At, a_atoms, Bt, b_atoms, tile_start, groups, dW=None
 # --------------------------------------- tokens sorted by expert and back ---
 # A small call costs less than its checks if those are careless: no message is
 # formatted and no Stream or device object is made unless something is wrong.
+# A given ``stream`` is made current for the call, so that what the call
+# allocates (outputs, scratch) belongs to the stream that uses it.
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
-def _queue(what, stream, *tensors) -> int:
-    """The stream to queue on, after checking that all tensors (None skipped)
-    are on one device and that it is the current one."""
+def _queue(what, *tensors) -> int:
+    """The current stream, after checking that all tensors (None skipped) are
+    on the current device."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise MoEError(f"{what}: every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _addr(t):
@@ -703,12 +705,15 @@ def moe_sort_rows(x, dst_of, rows=None, out=None, dev_err=None, stream=None):
     """x [T][d] (bf16, fp16 or fp32; row stride may exceed d) -> xs [rows][d]
     with xs[dst_of[t][k]] = x[t]; rows defaults to T*K.  Rows of a given
     ``out`` that no pair points at stay as they were (undefined in a new one)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_sort_rows(x, dst_of, rows, out, dev_err)
     what = "moe_sort_rows"
     T, K = _table(what, dst_of)
     dt = _row_type(what, x)
     d = _width(what, "x", x)[1]
     ldx = _ld(what, "x", x, T, d, x.dtype)
-    st = _queue(what, stream, x, dst_of, out, dev_err)
+    st = _queue(what, x, dst_of, out, dev_err)
     if out is None:
         out = x.new_empty((T * K if rows is None else rows, d))
         ldo = d
@@ -722,12 +727,15 @@ def moe_sort_rows(x, dst_of, rows=None, out=None, dev_err=None, stream=None):
 
 def moe_sort_rows_backward(dxs, dst_of, dx=None, dev_err=None, stream=None):
     """dxs [rows][d] -> dx [T][d] with dx[t] = sum_k dxs[dst_of[t][k]]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_sort_rows_backward(dxs, dst_of, dx, dev_err)
     what = "moe_sort_rows_backward"
     T, K = _table(what, dst_of)
     dt = _row_type(what, dxs)
     n, d = _width(what, "dxs", dxs)
     lds = _ld(what, "dxs", dxs, n, d, dxs.dtype)
-    st = _queue(what, stream, dxs, dst_of, dx, dev_err)
+    st = _queue(what, dxs, dst_of, dx, dev_err)
     if dx is None:
         dx = dxs.new_empty((T, d))
         ldx = d
@@ -742,13 +750,16 @@ def moe_sort_rows_backward(dxs, dst_of, dx=None, dev_err=None, stream=None):
 def moe_unsort_rows(y, dst_of, weight, out=None, dev_err=None, stream=None):
     """y [rows][d], weight fp32 [T][K] -> out [T][d] with
     out[t] = sum_k weight[t][k] y[dst_of[t][k]]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_unsort_rows(y, dst_of, weight, out, dev_err)
     what = "moe_unsort_rows"
     T, K = _table(what, dst_of)
     dt = _row_type(what, y)
     n, d = _width(what, "y", y)
     ldy = _ld(what, "y", y, n, d, y.dtype)
     _dense(what, "weight", weight, _F32, (T, K))
-    st = _queue(what, stream, y, dst_of, weight, out, dev_err)
+    st = _queue(what, y, dst_of, weight, out, dev_err)
     if out is None:
         out = y.new_empty((T, d))
         ldo = d
@@ -766,6 +777,10 @@ def moe_unsort_rows_backward(dout, y, dst_of, weight, dy=None, dweight=None, wan
     dy[dst_of[t][k]] = weight[t][k] dout[t] and dweight[t][k] = dout[t] .
     y[dst_of[t][k]]; either is None where it is not wanted.  Rows of a given
     ``dy`` that no pair points at stay as they were (undefined in a new one)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_unsort_rows_backward(dout, y, dst_of, weight, dy, dweight, want_dy,
+                                            want_dweight, dev_err)
     what = "moe_unsort_rows_backward"
     T, K = _table(what, dst_of)
     dt = _row_type(what, dout)
@@ -774,7 +789,7 @@ def moe_unsort_rows_backward(dout, y, dst_of, weight, dy=None, dweight=None, wan
     n = _width(what, "y", y)[0]
     ldy = _ld(what, "y", y, n, d, dout.dtype)
     _dense(what, "weight", weight, _F32, (T, K))
-    st = _queue(what, stream, dout, y, dst_of, weight, dy, dweight, dev_err)
+    st = _queue(what, dout, y, dst_of, weight, dy, dweight, dev_err)
     lddy = d
     if dy is not None:
         lddy = _ld(what, "dy", dy, n, d, dout.dtype)
@@ -806,6 +821,9 @@ def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None,
     """moe_combine that also keeps Y in 8 bits: Y fp32 [rows][d] ->
     (out fp32 [T][d], yq uint8 [rows][d], ys fp32 [rows][d/128]).  Rows that
     no pair points at stay as they were (undefined in new buffers)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, pow2, dev_err)
     what = "moe_combine_checkpoint"
     T, K = _table(what, dst_of)
     rows, d = _tiled(what, "Y", Y)
@@ -814,7 +832,7 @@ def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None,
     _dense(what, "u", u, _BF16, (T, d))
     if Y_shared is not None:
         _dense(what, "Y_shared", Y_shared, _F32, (T, d))
-    st = _queue(what, stream, Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, dev_err)
+    st = _queue(what, Y, dst_of, topk_gate, Y_shared, u, out, yq, ys, dev_err)
     if out is None:
         out = Y.new_empty((T, d))
     else:
@@ -839,6 +857,10 @@ def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, d
                                     dgate=None, want_dy=False, dev_err=None, stream=None):
     """dout fp32 [T][d] and the checkpoint (yq, ys) -> (dyq uint8 [T*K+T][d],
     dys [T*K+T][d/128], dy fp32 or None, dgate fp32 [T][K])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate,
+                                                   want_dy, dev_err)
     what = "moe_combine_checkpoint_backward"
     T, K = _table(what, dst_of)
     d = _tiled(what, "dout", dout)[1]
@@ -848,7 +870,7 @@ def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, d
     _dense(what, "topk_gate", topk_gate, _F32, (T, K))
     _dense(what, "yq", yq, _U8, (n, d))
     _dense(what, "ys", ys, _F32, (n, d // 128))
-    st = _queue(what, stream, dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate, dev_err)
+    st = _queue(what, dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate, dev_err)
     if dyq is None:
         dyq = yq.new_empty((rows, d))
     else:
@@ -888,6 +910,11 @@ def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base
     [T/seq_len] (None: ones).  Returns (dlogits fp32 [T][E], du fp32 [T][d] =
     du_base + dlogits . centroids, dcentroids fp32 [E][d] or None); du may be
     du_base."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f,
+                                      dloss, alpha, seq_len, dlogits, du, dcentroids, ws,
+                                      want_dcentroids, dev_err)
     what = "moe_route_backward"
     T, E = _width(what, "logits", logits)
     d = _width(what, "u", u)[1]
@@ -907,7 +934,7 @@ def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base
             _dense(what, "dloss", dloss, _F32, (T // seq_len,))
     if du_base is not None:
         _dense(what, "du_base", du_base, _F32, (T, d))
-    st = _queue(what, stream, dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f, dloss,
+    st = _queue(what, dgate, logits, topk_idx, topk_gate, u, centroids, du_base, f, dloss,
                 dlogits, du, dcentroids, ws, dev_err)
     if dlogits is None:
         dlogits = logits.new_empty((T, E))

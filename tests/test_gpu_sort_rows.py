@@ -240,7 +240,61 @@ def test_graph_replay_and_side_stream(cuda_dev):
     torch.cuda.current_stream().wait_stream(s)
     for a, b in zip(got, (xs, out, dy, dw)):
         assert torch.equal(a, b)
+    # given as an argument: new outputs belong to that stream
+    s.wait_stream(torch.cuda.current_stream())
+    out2 = moe.moe_unsort_rows(xs, dd, w, stream=s)
+    dy2, dw2 = moe.moe_unsort_rows_backward(out2, xs, dd, w, stream=s)
+    xs2 = moe.moe_sort_rows(x, dd, rows, stream=s)
+    dx2 = moe.moe_sort_rows_backward(xs2, dd, stream=s)
+    s.synchronize()
+    used = dd[dd >= 0].long()
+    assert torch.equal(out2, out) and torch.equal(dy2[used], dy[used]) and torch.equal(dw2, dw)
+    assert torch.equal(xs2[used], xs[used]) and dx2.shape == (T, d)
     del graph
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("d,ld,shift", [(64, 64, 1), (130, 131, 3), (96, 104, 4), (1024, 1032, 0), (7, 9, 2)])
+def test_rows_at_any_element_offset(cuda_dev, dtype, d, ld, shift):
+    """Views whose rows start at any element, and outputs that are such views:
+    the columns between rows stay as they were."""
+    T, K = 33, 3
+    dst, rows = _table(T, K, 0.2, 61)
+    dd = dst.to(cuda_dev)
+
+    def view(n, seed=None):
+        flat = torch.full((n * ld + 16,), 9.0, dtype=dtype, device=cuda_dev)
+        v = flat[shift:shift + n * ld].view(n, ld)[:, :d]
+        if seed is not None:
+            v.copy_(_mat(n, d, dtype, seed))
+        return flat, v
+
+    _, x = view(T, 62)
+    flat, xs = view(rows)
+    moe.moe_sort_rows(x, dd, rows, out=xs)
+    w = torch.rand(T, K, generator=torch.Generator().manual_seed(63)).to(cuda_dev)
+    fo, out = view(T)
+    moe.moe_unsort_rows(xs, dd, w, out=out)
+    fd, dy = view(rows)
+    _, dw = moe.moe_unsort_rows_backward(x, xs, dd, w, dy=dy)
+    fx, dx = view(T)
+    moe.moe_sort_rows_backward(xs, dd, dx=dx)
+    cx, cxs = x.clone(), xs.clone()
+    used = dd[dd >= 0].long()
+    assert torch.equal(cxs[used], moe.moe_sort_rows(cx, dd, rows)[used])
+    assert torch.equal(out, moe.moe_unsort_rows(cxs, dd, w))
+    dy2, dw2 = moe.moe_unsort_rows_backward(cx, cxs, dd, w)
+    assert torch.equal(dy[used], dy2[used])
+    assert torch.equal(dx, moe.moe_sort_rows_backward(cxs, dd))
+    # two access widths sum a dot product in two orders: d roundings of its terms each
+    t, k = torch.nonzero(dst >= 0, as_tuple=True)
+    mag = torch.zeros(T, K, dtype=torch.float64)
+    mag[t, k] = (cx.double().abs().cpu()[t] * cxs.double().abs().cpu()[dst[t, k].long()]).sum(1)
+    assert bool(((dw - dw2).double().cpu().abs() <= 2 * d * 2.0 ** -24 * mag).all())
+    for f, v, n in ((flat, xs, rows), (fo, out, T), (fd, dy, rows), (fx, dx, T)):
+        gap = torch.ones_like(f, dtype=torch.bool)
+        gap[shift:shift + n * ld].view(n, ld)[:, :d] = False
+        assert bool((f[gap] == 9.0).all())
 
 
 def test_refusals(cuda_dev):
