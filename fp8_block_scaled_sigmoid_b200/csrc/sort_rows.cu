@@ -26,10 +26,12 @@ constexpr int kSrWarps = 4;      // warps of a CTA, each with a piece of its own
 constexpr int kSrDotWarps = 16;  // most warps of a CTA whose warps share a token
 constexpr int kSrFlight = 8;     // accesses a lane has in flight: U columns x kSrFlight / U rows
 
-constexpr int kSrDotU = 2, kSrDotB = 2;  // columns and rows in flight there
+template <int N>
+constexpr int kSrDotU = N <= 2 ? 4 : 2;  // columns and rows in flight there
+constexpr int kSrDotB = 2;
 
-// N elements of T as one access of plain words (16 bytes, or a single element
-// where the rows' alignment allows no more), and as floats.
+// N elements of T as one access of plain words (16 bytes, or where the rows'
+// alignment allows no more 4 bytes or a single element), and as floats.
 template <typename T, int N>
 struct Row;
 
@@ -85,6 +87,17 @@ struct Row<T, 8> {
   static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
     return make_uint4(two(f[0], f[1], T{}), two(f[2], f[3], T{}), two(f[4], f[5], T{}), two(f[6], f[7], T{}));
   }
+};
+
+template <typename T>
+struct Row<T, 2> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ void get(uint32_t v, float (&f)[2]) {
+    const float2 p = two(v, T{});
+    f[0] = p.x;
+    f[1] = p.y;
+  }
+  static __device__ __forceinline__ uint32_t put(const float (&f)[2]) { return two(f[0], f[1], T{}); }
 };
 
 template <typename T>
@@ -181,7 +194,7 @@ __global__ void __launch_bounds__(32 * kSrDotWarps, 2) scatter_dot_kernel(
     int32_t* dev_err) {
   using R = Row<T, N>;
   using Raw = typename R::Raw;
-  constexpr int U = kSrDotU, B = kSrDotB;
+  constexpr int U = kSrDotU<N>, B = kSrDotB;
   extern __shared__ float dot[];  // [tokens][warps][K][8]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(32 * kSrWarps) gather_rows_kernel(
     int64_t ldo, int32_t* dev_err) {
   using R = Row<T, N>;
   using Raw = typename R::Raw;
-  constexpr int B = kSrFlight / U;
+  constexpr int B = N <= 2 ? 2 : kSrFlight / U;
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSrWarps + (threadIdx.x >> 5);
   const int64_t t = unit / items;
@@ -318,10 +331,12 @@ bool elem_aligned(const void* p, int e) {
   return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(e - 1)) == 0;
 }
 
-// Whether every row starting at p with stride ld can be accessed 16 bytes at a time.
-bool rows_aligned16(const void* p, int64_t ld, int e) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * e) % 16 == 0;
+// Low bits that a row of d elements at p with stride ld sets: none below 16
+// where 16-byte accesses fit.
+uintptr_t row_bits(const void* p, int64_t ld, int d, int e) {
+  return reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * e) | static_cast<uintptr_t>(static_cast<int64_t>(d) * e);
 }
+int access_bytes(uintptr_t bits, int e) { return bits % 16 == 0 ? 16 : (bits % 4 == 0 ? 4 : e); }
 
 moe_status check_shape(moe_dtype dt, int T, int K, int d, int64_t rows) {
   if (dt != MOE_BF16 && dt != MOE_F16 && dt != MOE_F32) return MOE_ERR_INVALID_ARG;
@@ -343,14 +358,25 @@ void with_unroll(int K, F&& fn) {
   else fn(Access<T, N, 4>{});
 }
 
-// fn(Access<T, N, U>) for the call's element type.  N is 16 bytes' worth where
-// every row involved is 16-byte aligned, else one element.  U columns of few
-// rows or one column of many: either way eight loads a lane are in flight.
+// fn(Access<T, N, U>) for the call's element type and the bytes (16, 4 or one
+// element) that every row involved is aligned to and made of.  U columns of
+// few rows or one column of many: either way eight loads a lane are in flight.
+// Narrow accesses take two rows of U columns: sort backward of 4096 x 8 rows in
+// bf16 takes 83 us at a width of 7168, 81 at 7002 and 146 at 7001.
 template <typename F>
-void with_access(moe_dtype dt, bool wide, int K, F&& fn) {
-  if (dt == MOE_BF16) wide ? with_unroll<__nv_bfloat16, 8>(K, fn) : fn(Access<__nv_bfloat16, 1, 4>{});
-  else if (dt == MOE_F16) wide ? with_unroll<__half, 8>(K, fn) : fn(Access<__half, 1, 4>{});
-  else wide ? with_unroll<float, 4>(K, fn) : fn(Access<float, 1, 4>{});
+void with_access(moe_dtype dt, int bytes, int K, F&& fn) {
+  if (dt == MOE_BF16) {
+    if (bytes == 16) with_unroll<__nv_bfloat16, 8>(K, fn);
+    else if (bytes == 4) fn(Access<__nv_bfloat16, 2, 8>{});
+    else fn(Access<__nv_bfloat16, 1, 4>{});
+  } else if (dt == MOE_F16) {
+    if (bytes == 16) with_unroll<__half, 8>(K, fn);
+    else if (bytes == 4) fn(Access<__half, 2, 8>{});
+    else fn(Access<__half, 1, 4>{});
+  } else {
+    if (bytes == 16) with_unroll<float, 4>(K, fn);
+    else fn(Access<float, 1, 4>{});
+  }
 }
 
 // One launch of the scatter without dot products.
@@ -381,10 +407,9 @@ moe_status gather(const void* src, moe_dtype dt, int64_t lds, int64_t rows, cons
   if (!elem_aligned(src, e) || !elem_aligned(out, e) || !elem_aligned(dst_of, 4) ||
       !elem_aligned(weight, 4))
     return MOE_ERR_ALIGN;
-  const bool wide = rows_aligned16(src, lds, e) && rows_aligned16(out, ldo, e) &&
-                    (static_cast<int64_t>(d) * e) % 16 == 0;
+  const int bytes = access_bytes(row_bits(src, lds, d, e) | row_bits(out, ldo, d, e), e);
   bool fits = true;
-  with_access(dt, wide, K, [&](auto access) {
+  with_access(dt, bytes, K, [&](auto access) {
     using E = typename decltype(access)::type;
     constexpr int N = decltype(access)::n, U = decltype(access)::u;
     auto kern = weighted ? gather_rows_kernel<E, N, U, true> : gather_rows_kernel<E, N, U, false>;
@@ -415,10 +440,9 @@ extern "C" moe_status moe_sort_rows(const void* x, moe_dtype dtype, int64_t ldx,
   if (!x || !dst_of || (rows > 0 && !xs)) return MOE_ERR_INVALID_ARG;
   const int e = elem_bytes(dtype);
   if (!elem_aligned(x, e) || !elem_aligned(xs, e) || !elem_aligned(dst_of, 4)) return MOE_ERR_ALIGN;
-  const bool wide = rows_aligned16(x, ldx, e) && rows_aligned16(xs, ldxs, e) &&
-                    (static_cast<int64_t>(d) * e) % 16 == 0;
+  const int bytes = access_bytes(row_bits(x, ldx, d, e) | row_bits(xs, ldxs, d, e), e);
   bool fits = true;
-  with_access(dtype, wide, K, [&](auto access) {
+  with_access(dtype, bytes, K, [&](auto access) {
     fits = launch_scatter<false>(access, x, ldx, dst_of, nullptr, T, K, d, xs, ldxs, rows, dev_err,
                                  static_cast<cudaStream_t>(stream));
   });
@@ -459,10 +483,10 @@ extern "C" moe_status moe_unsort_rows_backward(const void* dout, moe_dtype dtype
   if (!elem_aligned(dout, e) || !elem_aligned(y, e) || !elem_aligned(dy, e) ||
       !elem_aligned(dst_of, 4) || !elem_aligned(weight, 4) || !elem_aligned(dweight, 4))
     return MOE_ERR_ALIGN;
-  const bool wide = rows_aligned16(dout, ldo, e) && (!dy || rows_aligned16(dy, lddy, e)) &&
-                    (!dweight || rows_aligned16(y, ldy, e)) && (static_cast<int64_t>(d) * e) % 16 == 0;
+  const int bytes = access_bytes(row_bits(dout, ldo, d, e) | (dy ? row_bits(dy, lddy, d, e) : 0) |
+                                     (dweight ? row_bits(y, ldy, d, e) : 0), e);
   bool fits = true;
-  with_access(dtype, wide, K, [&](auto access) {
+  with_access(dtype, bytes, K, [&](auto access) {
     using A = decltype(access);
     using E = typename A::type;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -470,7 +494,7 @@ extern "C" moe_status moe_unsort_rows_backward(const void* dout, moe_dtype dtype
       fits = launch_scatter<true>(access, dout, ldo, dst_of, weight, T, K, d, dy, lddy, rows, dev_err, st);
       return;
     }
-    const Shape sh = dot_shape(T, K, sr_items(d, 32 * A::n * kSrDotU));
+    const Shape sh = dot_shape(T, K, sr_items(d, 32 * A::n * kSrDotU<A::n>));
     scatter_dot_kernel<E, A::n><<<static_cast<unsigned>(sh.grid), sh.block, sh.smem, st>>>(
         static_cast<const E*>(dout), ldo, dst_of, weight, T, K, d, static_cast<const E*>(y), ldy,
         static_cast<E*>(dy), lddy, rows, dweight, dev_err);

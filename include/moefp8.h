@@ -504,7 +504,7 @@ moe_status moe_combine(const float* Y, const int32_t* dst_of, const float* topk_
  * Products and sums are fp32 (k ascending), rounded once to dtype; a call's
  * result does not depend on timing.  No buffer written may overlap one read.
  * Pointers and leading dimensions need the element's own alignment only
- * (16-byte aligned rows take the faster path).
+ * (rows of whole 16-byte pieces, aligned to them, are fastest, 4-byte ones next).
  * Limits: d >= 1, 0 <= K <= 32, ld >= d, rows < 2^31.
  * =========================================================================== */
 
