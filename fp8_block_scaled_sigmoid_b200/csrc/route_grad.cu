@@ -10,13 +10,15 @@
 //     loss.  No division by a sum that may be tiny; 1 - s is 1 / (1 + e^z).
 //  2. product_kernel -- du = du_base + dz C and dC = dz^T u on the tensor
 //     cores.  u and C are bf16 as they are; dz is fp32, so it is split into
-//     three bf16 terms (hi + mid + lo holds its 24 bits) and every 64 deep
-//     block of the product takes three MMAs.  Two terms would lose 2^-17 of a
-//     gradient, which the router keeps in high precision.
+//     three bf16 terms (hi + mid + lo holds its 24 bits) and every 16 deep step
+//     of the product takes three MMAs.  Two terms would lose 2^-17 of a
+//     gradient, which the router keeps in high precision.  For many tokens du
+//     takes scaled half operands and two terms instead (half_centroids_kernel).
 //  3. The partial tiles of dC, whose depth T is split over the CTAs, are added
 //     in a fixed order, by two spare warps of du's CTAs while those work (or
 //     by reduce_kernel where du is not wanted).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -41,13 +43,74 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// What a product takes of dz: bf16 terms [3][T][E] (hi + mid + lo = dz), and
+// for du half terms [2][T][E] of dz 2^-k_e 2^m_t (see half_centroids_kernel).
+struct Terms {
+  uint16_t* bf16;         // NULL: not wanted
+  uint16_t* half;
+  const float* cent_inv;  // [E] 2^-k_e
+  float* row_scale;       // [T] 2^-m_t
+};
+
+// 2^(14 - floor(log2 max)): scales values of magnitude up to max below 2^15.
+__device__ __forceinline__ float scale_to_2_14(float max) {
+  const int e = static_cast<int>(__float_as_uint(max) >> 23) - 127;
+  const int m = max > 0.f ? min(126, 14 - e) : 0;  // 14 - 128 at least
+  return __uint_as_float(static_cast<uint32_t>(m + 127) << 23);
+}
+// The inverse of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(0x7F000000u - __float_as_uint(p)); }
+
+// du with half operands: half has three more mantissa bits than bf16, so two
+// terms of dz hold 22 bits and more, where bf16 takes three terms for 24 -- a
+// third of the tensor core's work less.  Half's narrow exponent is met by exact
+// powers of two: centroid e is scaled by 2^k_e so that its largest element
+// reaches [2^14, 2^15), which dz[.][e] undoes, and token t's row of dz by 2^m_t
+// in the same way, which the epilogue undoes.  What half's smallest step then
+// loses is 2^-39 of the centroid's, or the row's, largest element.  One CTA an
+// expert.
+__global__ void __launch_bounds__(256) half_centroids_kernel(const uint16_t* __restrict__ cent, int d,
+                                                             uint16_t* __restrict__ out,
+                                                             float* __restrict__ cent_inv) {
+  __shared__ float part[8];
+  launch_dependents();
+  const uint4* row = reinterpret_cast<const uint4*>(cent + static_cast<int64_t>(blockIdx.x) * d);
+  uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(blockIdx.x) * d);
+  float m = 0.f;
+  for (int v = threadIdx.x; v < d / 8; v += 256) {
+    const uint4 w = __ldg(row + v);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+  const float k = scale_to_2_14(m);
+  for (int v = threadIdx.x; v < d / 8; v += 256) {
+    const uint4 w = __ldg(row + v);
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(__fmul_rn(k, __uint_as_float(x[i] << 16)), __fmul_rn(k, __uint_as_float(x[i] & 0xFFFF0000u)));
+      x[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    dst[v] = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  if (threadIdx.x == 0) cent_inv[blockIdx.x] = pow2_inverse(k);
+}
+
 // Lane l owns experts 4 l + 128 i .. + 3, i < Q: 16-byte accesses (E % 16 == 0).
 template <int Q>
 __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     const float* __restrict__ dgate, const float* __restrict__ logits,
     const int32_t* __restrict__ idx, const float* __restrict__ gate, int T, int E, int K,
     const float* __restrict__ f, const float* __restrict__ dloss, int seq_len, float alpha,
-    float* __restrict__ dz, uint16_t* __restrict__ terms, int32_t* dev_err) {
+    float* __restrict__ dz, const Terms terms, int32_t* dev_err) {
   __shared__ float gate_sm[kRgThreads / 32 * 128 * Q];
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRgThreads / 32) + (threadIdx.x >> 5);
@@ -144,18 +207,54 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     if (e >= E) continue;
     float r[4] = {out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
     if (dz) *reinterpret_cast<float4*>(dz + t * E + e) = make_float4(r[0], r[1], r[2], r[3]);
-    if (terms) {
+    if (terms.bf16) {
       // hi + mid + lo = out: each difference is exact
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         const __nv_bfloat162 h0 = __floats2bfloat162_rn(r[0], r[1]), h1 = __floats2bfloat162_rn(r[2], r[3]);
-        *reinterpret_cast<uint2*>(terms + m * plane + t * E + e) =
+        *reinterpret_cast<uint2*>(terms.bf16 + m * plane + t * E + e) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
         r[0] = __fsub_rn(r[0], __low2float(h0));
         r[1] = __fsub_rn(r[1], __high2float(h0));
         r[2] = __fsub_rn(r[2], __low2float(h1));
         r[3] = __fsub_rn(r[3], __high2float(h1));
       }
+    }
+  }
+  if (!terms.half) return;
+  wait_predecessor();  // half_centroids_kernel's scales
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int e = 128 * i + 4 * lane;
+    const float4 c = e < E ? *reinterpret_cast<const float4*>(terms.cent_inv + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    out[4 * i] = __fmul_rn(out[4 * i], c.x);
+    out[4 * i + 1] = __fmul_rn(out[4 * i + 1], c.y);
+    out[4 * i + 2] = __fmul_rn(out[4 * i + 2], c.z);
+    out[4 * i + 3] = __fmul_rn(out[4 * i + 3], c.w);
+#pragma unroll
+    for (int j = 4 * i; j < 4 * i + 4; ++j) top = fmaxf(top, fabsf(out[j]));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float m_t = scale_to_2_14(top);
+  if (lane == 0) terms.row_scale[t] = pow2_inverse(m_t);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int e = 128 * i + 4 * lane;
+    if (e >= E) continue;
+    float r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = __fmul_rn(m_t, out[4 * i + j]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const __half2 h0 = __floats2half2_rn(r[0], r[1]), h1 = __floats2half2_rn(r[2], r[3]);
+      *reinterpret_cast<uint2*>(terms.half + m * plane + t * E + e) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+      r[0] = __fsub_rn(r[0], __low2float(h0));
+      r[1] = __fsub_rn(r[1], __high2float(h0));
+      r[2] = __fsub_rn(r[2], __low2float(h1));
+      r[3] = __fsub_rn(r[3], __high2float(h1));
     }
   }
 }
@@ -166,25 +265,28 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 //   du: A = dz as stored (M = tokens, depth = experts), B = the centroids
 //   dC: A = dz transposed, also MN-major (M = experts, depth = tokens), B = u
 // Tiles of 128 x 256 over depth blocks of 32.  One thread issues the TMA
-// loads of a ring of 40 KB stages (24 KB of A, all three terms in one box or
-// two; 16 KB of B), one thread issues the MMAs, eight warps add finished
+// loads of a ring of stages (the terms of A in one box or two, 8 KB each, and
+// 16 KB of B), one thread issues the MMAs, eight warps add finished
 // accumulators in registers: the two TMEM accumulators alternate every 128
 // deep, so that a tensor-core sum, whose additions may truncate, stays 24
 // steps long and the rest is rounded fp32 additions.  The depth blocks of all
 // tiles form one line that is cut evenly over the CTAs (for du at tile
 // borders): every SM gets the same work whatever the shape, and dC's few
-// tiles still fill the GPU.
-// du is bound by reading the base and writing du in fp32 (HBM), dC by the
-// tensor cores.  Issuing a TMA load takes its thread about 70 cycles: ten a
-// stage held both back, hence the boxes of three terms.  Each epilogue warp
-// has 32 x 32 patches of its own in shared memory, which TMA fills with the
-// base ahead of time and empties into the result.
+// tiles still fill the GPU.  An epilogue warp has 32 x 32 patches of its own in
+// shared memory, which TMA fills with the base ahead of time and empties into
+// the result.
+// dC is bound by the tensor cores (16384 x 384 x 7168 in three terms: 190 us,
+// 1.42 PFLOP/s with the power cap holding the clock near 1.5 GHz).  du reads the
+// base and writes du besides (4096 x 7168 fp32: 36 us at the copy rate) and
+// takes 58 us there: its operand loads wait behind those streams; deeper
+// patches, contiguous operands, narrower tiles, L2 prefetches and pairs of CTAs
+// (cta_group::2) were all tried and gave nothing more.
+constexpr uint32_t kFmtF16 = 0;  // kind::f16
 constexpr int kPrM = 128, kPrN = 256, kPrK = 32;
 constexpr int kPrChunk = 4;                       // depth blocks per accumulator
 constexpr int kPrTerm = kPrM * kPrK * 2;          // bytes of one term's A block
 constexpr int kPrSlab = 64 * kPrK * 2;            // 64 columns of an MN-major operand
 constexpr int kPrB = kPrK * kPrN * 2;
-constexpr int kPrStage = 3 * kPrTerm + kPrB;
 constexpr int kPrEpiWarps = 8;
 constexpr int kPrThreads = 128 + 32 * kPrEpiWarps;  // TMA, MMA and two spare warps; the epilogue
 // launched with 168 registers a thread; 128 x 72 + 256 x 216 = 384 x 168
@@ -192,13 +294,14 @@ constexpr int kPrRegsCtl = 72, kPrRegsEpi = 216;
 constexpr int kPrPatch = 32 * 32 * 4;
 constexpr uint32_t kPrTmemCols = 2 * kPrN;
 // du keeps three patches a warp (two loads of the base in flight while one is
-// used) and a ring of three stages, dC two patches and four stages.
-template <bool A_MN>
-constexpr int kPrStages = A_MN ? 4 : 3;
-template <bool A_MN>
-constexpr int kPrPatches = A_MN ? 2 : 3;
-template <bool A_MN>
-constexpr int kPrSmem = 1024 + kPrStages<A_MN> * kPrStage + kPrPatches<A_MN> * kPrEpiWarps * kPrPatch + 512;
+// used) and, with three terms, a stage less than dC.
+template <bool A_MN, int TERMS>
+struct Ring {
+  static constexpr int kStage = TERMS * kPrTerm + kPrB;
+  static constexpr int kStages = A_MN || TERMS == 2 ? 4 : 3;
+  static constexpr int kPatches = A_MN ? 2 : 3;
+  static constexpr int kSmem = 1024 + kStages * kStage + kPatches * kPrEpiWarps * kPrPatch + 512;
+};
 
 // Depth blocks up to which dC's tiles stay whole (T <= 512).
 constexpr int kPrShort = 16;
@@ -218,6 +321,7 @@ struct ProductArgs {
   int per;       // depth blocks of a CTA; 0: whole tiles, evenly
   int has_base;
   int after_dc;  // du launched behind dC
+  const float* row_scale;  // of half terms
   Parts parts;   // du: dC's parts to add (tiles 0: none)
   int32_t* dev_err;
 };
@@ -318,16 +422,17 @@ __global__ void __launch_bounds__(64) reduce_kernel(const Parts parts) {
   add_parts(parts, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
-template <bool A_MN>
+template <bool A_MN, int TERMS>
 __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
     const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
     const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmOut,
     const __grid_constant__ CUtensorMap tmPart, const ProductArgs args) {
-  constexpr int kStages = kPrStages<A_MN>, kPatches = kPrPatches<A_MN>;
+  using R = Ring<A_MN, TERMS>;
+  constexpr int kStages = R::kStages, kPatches = R::kPatches;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* patches = ring + kStages * kPrStage;
+  uint8_t* patches = ring + kStages * R::kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(patches + kPatches * kPrEpiWarps * kPrPatch);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
@@ -394,12 +499,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
             live = false;
             break;
           }
-          uint8_t* sA = ring + s * kPrStage;
-          uint8_t* sB = sA + 3 * kPrTerm;
-          mbar_arrive_expect_tx(&full[s], kPrStage);
+          uint8_t* sA = ring + s * R::kStage;
+          uint8_t* sB = sA + TERMS * kPrTerm;
+          mbar_arrive_expect_tx(&full[s], R::kStage);
           if (A_MN) {  // [64 experts][term][depth][64]
             tma_load_3d(sA, &tmA, &full[s], g.m0, kb * kPrK, 0);
-            tma_load_3d(sA + 3 * kPrSlab, &tmA, &full[s], g.m0 + 64, kb * kPrK, 0);
+            tma_load_3d(sA + TERMS * kPrSlab, &tmA, &full[s], g.m0 + 64, kb * kPrK, 0);
           } else {     // [term][row][depth]
             tma_load_3d(sA, &tmA, &full[s], kb * kPrK, g.m0, 0);
           }
@@ -413,7 +518,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
         mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, args.dev_err);
     } else if (warp == 1 && lane == 0) {
       // ----------------------------------------------------------- MMA issuer
-      const uint32_t idesc = instr_desc(kFmtBF16, kFmtBF16, kPrM, kPrN) | (A_MN ? 1u << 15 : 0u) | (1u << 16);
+      constexpr uint32_t kFmt = TERMS == 2 ? kFmtF16 : kFmtBF16;
+      const uint32_t idesc = instr_desc(kFmt, kFmt, kPrM, kPrN) | (A_MN ? 1u << 15 : 0u) | (1u << 16);
       constexpr uint64_t kStepA = A_MN ? 2048 >> 4 : 32 >> 4;  // 16 deep
       constexpr uint64_t kStepB = 2048 >> 4;
       int it = 0, ch = 0;
@@ -437,15 +543,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
               break;
             }
             tc_fence_after();
-            const uint32_t sA = smem_u32(ring + s * kPrStage);
-            const uint64_t bd = smem_desc_mn_sw128(sA + 3 * kPrTerm, kPrSlab);
+            const uint32_t sA = smem_u32(ring + s * R::kStage);
+            const uint64_t bd = smem_desc_mn_sw128(sA + TERMS * kPrTerm, kPrSlab);
 #pragma unroll
             for (int k = 0; k < kPrK / 16; ++k)
 #pragma unroll
-              for (int j = 2; j >= 0; --j) {  // the smallest term first
-                const uint64_t ad = A_MN ? smem_desc_mn_sw128(sA + j * kPrSlab, 3 * kPrSlab)
+              for (int j = TERMS - 1; j >= 0; --j) {  // the smallest term first
+                const uint64_t ad = A_MN ? smem_desc_mn_sw128(sA + j * kPrSlab, TERMS * kPrSlab)
                                          : smem_desc_sw64(sA + j * kPrTerm);
-                mma_f16(acc, ad + k * kStepA, bd + k * kStepB, idesc, (kb > kc || k > 0 || j < 2) ? 1u : 0u);
+                mma_f16(acc, ad + k * kStepA, bd + k * kStepB, idesc, (kb > kc || k > 0 || j < TERMS - 1) ? 1u : 0u);
               }
             mma_commit(&empty[s]);
           }
@@ -494,6 +600,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
     for (int pos = start; pos < end && ok;) {
       const Segment g = next_segment(args, start, pos, end);
       pos += g.k1 - g.k0;
+      // the row's power of two back
+      float row_scale = 1.f;
+      if (TERMS == 2 && g.m0 + quarter * 32 + lane < args.M) row_scale = __ldg(args.row_scale + g.m0 + quarter * 32 + lane);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -537,6 +646,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
         for (int c = 0; c < 8; ++c) {
           float4* at = reinterpret_cast<float4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4));
           float4 v = make_float4(acc[32 * b + 4 * c], acc[32 * b + 4 * c + 1], acc[32 * b + 4 * c + 2], acc[32 * b + 4 * c + 3]);
+          if (TERMS == 2) {
+            v.x = __fmul_rn(row_scale, v.x);
+            v.y = __fmul_rn(row_scale, v.y);
+            v.z = __fmul_rn(row_scale, v.z);
+            v.w = __fmul_rn(row_scale, v.w);
+          }
           if (has_base) add4(v, *at);
           *at = v;
         }
@@ -563,17 +678,33 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   if (warp == 1) tmem_dealloc(tmem, kPrTmemCols);
 }
 
-template <int Q>
-void launch_dlogits(cudaStream_t st, const float* dgate, const float* logits, const int32_t* idx,
-                    const float* gate, int T, int E, int K, const float* f, const float* dloss,
-                    int seq_len, float alpha, float* dz, uint16_t* terms, int32_t* dev_err) {
-  const int blocks = (T + kRgThreads / 32 - 1) / (kRgThreads / 32);
-  dlogits_kernel<Q><<<blocks, kRgThreads, 0, st>>>(dgate, logits, idx, gate, T, E, K, f, dloss,
-                                                   seq_len, alpha, dz, terms, dev_err);
+// Launches a kernel, behind: before the one ahead of it has ended.
+template <typename... P, typename... A>
+bool launch(void (*kern)(P...), int64_t grid, int block, int smem, bool behind, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
+// Tokens above which du takes half operands: the call takes 567 us against 628
+// at 16384 tokens and 384 experts, the same at 4096 (118 against 119) and more
+// below (50 against 43 at 1024), where converting the centroids costs what the
+// product saves.
+constexpr int kHalfAbove = 4096;
+
 struct Plan {
-  size_t terms, parts;  // workspace bytes
+  // workspace bytes: dz in bf16 and in half terms, the centroids in half, the
+  // scales of both, dC's parts
+  size_t bf16, half, cent, cent_inv, row_scale, parts, all;
+  bool half_du;
   int du_units, du_kb, du_mt, du_ctas;
   int dc_units, dc_kb, dc_mt, dc_per, dc_ctas;
   bool fits;
@@ -598,8 +729,15 @@ Plan make_plan(int T, int d, int E) {
   const int64_t per = (dc + sms - 1) / sms;
   p.dc_per = static_cast<int>(tk <= kPrShort ? (per + tk - 1) / (tk ? tk : 1) * tk : per);
   p.dc_ctas = p.dc_per ? static_cast<int>((dc + p.dc_per - 1) / p.dc_per) : 0;
-  p.terms = (static_cast<size_t>(T) * E * 2 * 3 + 255) / 256 * 256;
+  auto bytes = [](int64_t a, int64_t b, int64_t c) { return (static_cast<size_t>(a) * b * c + 255) / 256 * 256; };
+  p.half_du = T > kHalfAbove;
+  p.bf16 = bytes(T, E, 3 * 2);
+  p.half = p.half_du ? bytes(T, E, 2 * 2) : 0;
+  p.cent = p.half_du ? bytes(E, d, 2) : 0;
+  p.cent_inv = p.half_du ? bytes(E, 4, 1) : 0;
+  p.row_scale = p.half_du ? bytes(T, 4, 1) : 0;
   p.parts = static_cast<size_t>(2) * p.dc_ctas * kPrM * kPrN * sizeof(float);
+  p.all = p.bf16 + p.half + p.cent + p.cent_inv + p.row_scale + p.parts;
   return p;
 }
 
@@ -609,27 +747,13 @@ bool grant_smem() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (dev >= 0 && dev < 64 && done[dev]) return true;
-  if (cudaFuncSetAttribute(product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<true>) != cudaSuccess ||
-      cudaFuncSetAttribute(product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<false>) != cudaSuccess)
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (cudaFuncSetAttribute(product_kernel<true, 3>, attr, Ring<true, 3>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(product_kernel<false, 3>, attr, Ring<false, 3>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(product_kernel<false, 2>, attr, Ring<false, 2>::kSmem) != cudaSuccess)
     return false;
   if (dev >= 0 && dev < 64) done[dev] = true;
   return true;
-}
-
-// Launches a kernel that may start before the one ahead of it has ended.
-template <typename... P, typename... A>
-bool launch_behind(void (*kern)(P...), int grid, int block, int smem, cudaStream_t st, const A&... args) {
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -651,7 +775,7 @@ extern "C" moe_status moe_route_backward_workspace_size(int T, int d, int E, siz
   if (s != MOE_OK) return s;
   const moe::Plan p = moe::make_plan(T, d, E);
   if (!p.fits) return MOE_ERR_UNSUPPORTED;
-  *bytes = p.terms + p.parts;
+  *bytes = p.all;
   return MOE_OK;
 }
 
@@ -685,44 +809,67 @@ extern "C" moe_status moe_route_backward(
   if (!aligned16(ws)) return MOE_ERR_ALIGN;
   const Plan plan = make_plan(T, d, E);
   if (!plan.fits) return MOE_ERR_UNSUPPORTED;
-  uint16_t* terms = static_cast<uint16_t*>(ws);
-  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.terms);
-  const bool products = du || dcentroids;
-  if (products && !grant_smem()) return MOE_ERR_CUDA;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  auto take = [&](size_t n) {
+    uint8_t* p = at;
+    at += n;
+    return p;
+  };
+  uint16_t* bf16_terms = reinterpret_cast<uint16_t*>(take(plan.bf16));
+  uint16_t* half_terms = reinterpret_cast<uint16_t*>(take(plan.half));
+  uint16_t* half_cent = reinterpret_cast<uint16_t*>(take(plan.cent));
+  float* cent_inv = reinterpret_cast<float*>(take(plan.cent_inv));
+  float* row_scale = reinterpret_cast<float*>(take(plan.row_scale));
+  float* parts = reinterpret_cast<float*>(take(plan.parts));
+  const bool half_du = du && plan.half_du;
+  if ((du || dcentroids) && !grant_smem()) return MOE_ERR_CUDA;
+  if (half_du && !launch(half_centroids_kernel, E, 256, 0, false, st, centroids, d, half_cent, cent_inv))
+    return MOE_ERR_CUDA;
+  const Terms terms{dcentroids || (du && !half_du) ? bf16_terms : nullptr, half_du ? half_terms : nullptr, cent_inv,
+                    row_scale};
   const int Q = (E + 127) / 128;
-  auto go = Q <= 1 ? launch_dlogits<1> : Q <= 2 ? launch_dlogits<2> : Q <= 3 ? launch_dlogits<3>
-          : Q <= 4 ? launch_dlogits<4> : launch_dlogits<8>;
-  go(st, dgate, logits, topk_idx, topk_gate, T, E, K, f, dloss, seq_len, alpha, dlogits,
-     products ? terms : nullptr, dev_err);
-  MOE_CUDA_CHECK_LAUNCH();
+  auto dlogits_q = Q <= 1 ? dlogits_kernel<1> : Q <= 2 ? dlogits_kernel<2> : Q <= 3 ? dlogits_kernel<3>
+                 : Q <= 4 ? dlogits_kernel<4> : dlogits_kernel<8>;
+  constexpr int kWarps = kRgThreads / 32;
+  if (!launch(dlogits_q, (static_cast<int64_t>(T) + kWarps - 1) / kWarps, kRgThreads, 0, half_du, st, dgate, logits,
+              topk_idx, topk_gate, T, E, K, f, dloss, seq_len, alpha, dlogits, terms, dev_err))
+    return MOE_ERR_CUDA;
 
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const auto fp16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const uint64_t rd = static_cast<uint64_t>(d) * 4, rz = static_cast<uint64_t>(E) * 2;
-  const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), 3}, stride[2] = {rz, rz * T};
-  const uint32_t box_mn[3] = {64, kPrK, 3}, box_k[3] = {kPrK, kPrM, 3};
+  const uint64_t stride[2] = {rz, rz * T};
   CUtensorMap a, b, in, out, part;
   Parts left{};  // dC's parts that are still to be added
   if (dcentroids) {
-    if (!moe_make_tmap_3d(&a, terms, bf16, extent, stride, box_mn, 128) ||
+    const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), 3};
+    const uint32_t box[3] = {64, kPrK, 3};
+    if (!moe_make_tmap_3d(&a, bf16_terms, bf16, extent, stride, box, 128) ||
         !moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
         !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
         !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, Parts{}, dev_err};
-    if (!launch_behind(product_kernel<true>, plan.dc_ctas, kPrThreads, kPrSmem<true>, st, a, b, out, out, part, args))
+    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, nullptr, Parts{}, dev_err};
+    if (!launch(product_kernel<true, 3>, plan.dc_ctas, kPrThreads, Ring<true, 3>::kSmem, true, st, a, b, out, out, part, args))
       return MOE_ERR_CUDA;
     if (plan.dc_per % plan.dc_kb != 0)  // else every CTA's tiles are whole
       left = Parts{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
   }
   if (du) {
-    if (!moe_make_tmap_3d(&a, terms, bf16, extent, stride, box_k, 64) ||
-        !moe_make_tmap_2d(&b, centroids, bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK) ||
+    const uint32_t n = half_du ? 2 : 3;
+    const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), n};
+    const uint32_t box[3] = {kPrK, kPrM, n};
+    if (!moe_make_tmap_3d(&a, half_du ? half_terms : bf16_terms, half_du ? fp16 : bf16, extent, stride, box, 64) ||
+        !moe_make_tmap_2d(&b, half_du ? half_cent : centroids, half_du ? fp16 : bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK) ||
         !moe_make_tmap_2d(&in, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
         !moe_make_tmap_2d(&out, du, fp32, d, T, rd, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, dcentroids ? 1 : 0, left, dev_err};
-    if (!launch_behind(product_kernel<false>, plan.du_ctas, kPrThreads, kPrSmem<false>, st, a, b, in, out, out, args))
-      return MOE_ERR_CUDA;
+    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, dcentroids ? 1 : 0, row_scale,
+                           left, dev_err};
+    const bool ok = half_du
+        ? launch(product_kernel<false, 2>, plan.du_ctas, kPrThreads, Ring<false, 2>::kSmem, true, st, a, b, in, out, out, args)
+        : launch(product_kernel<false, 3>, plan.du_ctas, kPrThreads, Ring<false, 3>::kSmem, true, st, a, b, in, out, out, args);
+    if (!ok) return MOE_ERR_CUDA;
   } else if (left.tiles) {
     const int groups = left.tiles * (kPrM / 4);
     reduce_kernel<<<std::min(groups, 8 * moe_num_sms()), 64, 0, st>>>(left);

@@ -83,7 +83,7 @@ CASES = [
     # T, E, d, K, n_seq
     (1, 16, 128, 1, 0), (1, 256, 7168, 8, 1), (37, 16, 256, 4, 0), (129, 80, 384, 6, 3), (128, 48, 640, 16, 4),
     (200, 256, 7168, 8, 0), (300, 384, 1152, 6, 2), (257, 1024, 256, 32, 1), (1000, 128, 2048, 2, 8),
-    (2500, 272, 896, 8, 5),
+    (2500, 272, 896, 8, 5), (4097, 64, 512, 4, 0), (4608, 272, 384, 8, 4),
 ]
 
 
@@ -116,6 +116,42 @@ def test_extreme_logits(cuda_dev):
     out = _call(c, 2)
     assert all(bool(torch.isfinite(t).all()) for t in out)
     _check(c, 2, out)
+
+
+def test_many_tokens_with_uneven_scales(cuda_dev):
+    """Above 4096 tokens du is the product of scaled half operands: centroids
+    and gradient rows of very different sizes, zero ones among them.  Two half
+    terms hold dz within 2^-23 of a value and 2^-39 of its row's largest
+    contribution top = max_e |dz_e| max|C_e| (half's smallest step is 2^-24,
+    the row's largest value at least 2^14), a half centroid within 2^-39 of
+    its largest element."""
+    T, E, d, K = 4100, 48, 384, 4
+    c = _case(T, E, d, K, 4, 17, cuda_dev)
+    c["cent"][3] = 0.0
+    c["cent"][5] *= 2.0 ** 30
+    c["cent"][7] *= 2.0 ** -60
+    c["cent"][9, 100] = 3.0e4
+    c["dgate"][10:20] = 0.0
+    c["dgate"][20:30] *= 1e-20
+    c["dgate"][30:40] *= 1e15
+    c = {k: (v if k != "f" else None) for k, v in c.items()}
+    c["dloss"] = None
+    dlogits, du, dc = _call(c, 0)
+    dz, cent = dlogits.double(), c["cent"].double()
+    ref = c["base"].double() + dz @ cent.double()
+    top = (dz.abs() * cent.abs().amax(1)).amax(1, keepdim=True)
+    bound = ((3 * E + 8) * 2.0 ** -23 * (dz.abs() @ cent.abs()) + 2.0 ** -23 * (ref.abs() + c["base"].double().abs())
+             + 3 * E * 2.0 ** -39 * top)
+    assert bool(((du.double() - ref).abs() <= bound).all())
+    assert torch.equal(du[10:20], c["base"][10:20])
+    ref = dz.T @ c["u"].double()
+    bound = (3 * T + 8) * 2.0 ** -23 * (dz.abs().T @ c["u"].double().abs()) + 2.0 ** -23 * ref.abs()
+    assert bool(((dc.double() - ref).abs() <= bound).all())
+    # a NaN stays in its token's row of du
+    c["dgate"][50, 1] = float("nan")
+    du2 = _call(c, 0)[1]
+    rest = torch.arange(T, device=cuda_dev) != 50
+    assert torch.equal(du2[rest], du[rest]) and bool(torch.isnan(du2[50]).all())
 
 
 def test_parts_alone(cuda_dev):
