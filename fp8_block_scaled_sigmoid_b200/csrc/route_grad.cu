@@ -303,8 +303,9 @@ struct Ring {
   static constexpr int kSmem = 1024 + kStages * kStage + kPatches * kPrEpiWarps * kPrPatch + 512;
 };
 
-// Depth blocks up to which dC's tiles stay whole (T <= 512).
-constexpr int kPrShort = 16;
+// CTAs of du from which its spare warps add dC's parts, and the most parts a
+// tile may have there (one thread adds them in turn).
+constexpr int kPrAdders = 100, kPrAdds = 4;
 
 // The parts of dC's tiles: CTA c worked on depth blocks [c * per, (c + 1) *
 // per) of the line; its part of its first tile is slot 2 c, of its last 2 c + 1.
@@ -385,41 +386,42 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 }
 
 // Adds the parts of every tile that more than one CTA worked on, CTA by CTA;
-// 64 threads take four rows of a tile at a time.
+// 64 threads take ROWS rows of a tile at a time and read AHEAD parts ahead.
+template <int ROWS, int AHEAD>
 __device__ __forceinline__ void add_parts(const Parts& a, int worker, int workers, int thread) {
-  constexpr int kRows = 4;
-  for (int g = worker; g < a.tiles * (kPrM / kRows); g += workers) {
-    const int tile = g / (kPrM / kRows), r0 = g % (kPrM / kRows) * kRows;
+  for (int g = worker; g < a.tiles * (kPrM / ROWS); g += workers) {
+    const int tile = g / (kPrM / ROWS), r0 = g % (kPrM / ROWS) * ROWS;
     const int c0 = tile * a.KB / a.per, c1 = ((tile + 1) * a.KB - 1) / a.per;
     if (c0 == c1) continue;
     const int m = tile % a.mt * kPrM + r0, n = tile / a.mt * kPrN + 4 * thread;
-    if (m >= a.M || n >= a.N) continue;  // M is a multiple of four rows
-    auto at = [&](int c) {
-      const int slot = 2 * c + (c * a.per / a.KB == tile ? 0 : 1);
-      return reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(slot) * (kPrM * kPrN) + r0 * kPrN) + thread;
-    };
-    float4 sum[kRows], more[kRows];
-    const float4 *p = at(c0), *q = at(c0 + 1);
+    if (m >= a.M || n >= a.N) continue;  // M is a multiple of ROWS
+    float4 sum[ROWS];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) sum[r] = __ldg(p + r * (kPrN / 4));
+    for (int r = 0; r < ROWS; ++r) sum[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += AHEAD) {
+      float4 v[AHEAD][ROWS];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) more[r] = __ldg(q + r * (kPrN / 4));
-    for (int c = c0 + 1;;) {
+      for (int i = 0; i < AHEAD; ++i) {
+        const int slot = 2 * (c + i) + ((c + i) * a.per / a.KB == tile ? 0 : 1);
+        const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot) * kPrM + r0) * kPrN) + thread;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) add4(sum[r], more[r]);
-      if (++c > c1) break;
-      q = at(c);
+        for (int r = 0; r < ROWS; ++r) v[i][r] = c + i <= c1 ? __ldg(p + r * (kPrN / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) more[r] = __ldg(q + r * (kPrN / 4));
+      for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) add4(sum[r], v[i][r]);
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < ROWS; ++r)
       *reinterpret_cast<float4*>(a.out + static_cast<int64_t>(m + r) * a.N + n) = sum[r];
   }
 }
 
 __global__ void __launch_bounds__(64) reduce_kernel(const Parts parts) {
-  add_parts(parts, blockIdx.x, gridDim.x, threadIdx.x);
+  wait_predecessor();
+  launch_dependents();
+  add_parts<1, 8>(parts, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 template <bool A_MN, int TERMS>
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       mbar_wait(done, 0, nullptr, args.dev_err);
     } else if (!A_MN && warp >= 2) {
       if (args.after_dc) wait_predecessor();
-      if (args.parts.tiles) add_parts(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
+      if (args.parts.tiles) add_parts<4, 2>(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
     }
     __syncwarp();
   } else {
@@ -707,8 +709,40 @@ struct Plan {
   bool half_du;
   int du_units, du_kb, du_mt, du_ctas;
   int dc_units, dc_kb, dc_mt, dc_per, dc_ctas;
-  bool fits;
+  bool fits;   // 32-bit arithmetic
 };
+
+// How dC's tiles, each tk depth blocks deep, are cut: whole, into n equal parts
+// (one CTA each, the depth padded with blocks of zeros), or evenly along the
+// line of all tiles (a CTA may then end one tile and begin the next).  A choice
+// costs, in depth blocks of about half a microsecond: the longest CTA's blocks,
+// 4 for each tile or part it writes, and for adding n parts up n / 4 and 4 in
+// du's spare warps, 12 in a kernel of its own.  920 tokens x 384 experts x 1024
+// take 28 us so and 58 with every line cut evenly, 200 x 384 x 1408 16 us with
+// whole tiles and 25 in seven parts.
+void plan_dc(Plan& p, int64_t sms, int64_t tiles, int64_t tk) {
+  auto adding = [&](int64_t n) { return (p.du_ctas >= kPrAdders && n <= kPrAdds ? 4 : 12) + n / 4; };
+  int64_t kb = tk, per = tk * ((tiles + sms - 1) / sms), best = per + 4;
+  for (int64_t n = 2; n <= 32 && n * tiles <= sms && n <= tk; ++n) {
+    const int64_t part = (tk + n - 1) / n, cost = part + 4 + adding(n);
+    if (cost < best) {
+      best = cost;
+      kb = part * n;
+      per = part;
+    }
+  }
+  const int64_t even = (tiles * tk + sms - 1) / sms;
+  if (even > 0 && even + 8 + adding(tk / even + 2) < best) {
+    kb = tk;
+    per = even;
+  }
+  const int64_t units = tiles * kb;
+  p.fits = units < (1ll << 31) && per < (1ll << 31);
+  p.dc_units = static_cast<int>(units);
+  p.dc_kb = static_cast<int>(kb);
+  p.dc_per = static_cast<int>(per);
+  p.dc_ctas = per ? static_cast<int>((units + per - 1) / per) : 0;
+}
 
 Plan make_plan(int T, int d, int E) {
   Plan p;
@@ -716,19 +750,14 @@ Plan make_plan(int T, int d, int E) {
   const int64_t nt = (d + kPrN - 1) / kPrN;
   const int64_t tm = (static_cast<int64_t>(T) + kPrM - 1) / kPrM, tk = (static_cast<int64_t>(T) + kPrK - 1) / kPrK;
   const int64_t em = (E + kPrM - 1) / kPrM, ek = (E + kPrK - 1) / kPrK;
-  const int64_t du = tm * nt * ek, dc = em * nt * tk;
-  p.fits = du < (1ll << 31) && dc < (1ll << 31);
+  const int64_t du = tm * nt * ek;
   p.du_units = static_cast<int>(du);
   p.du_kb = static_cast<int>(ek);
   p.du_mt = static_cast<int>(tm);
   p.du_ctas = static_cast<int>(std::min(sms, tm * nt));
-  p.dc_units = static_cast<int>(dc);
-  p.dc_kb = static_cast<int>(tk);
   p.dc_mt = static_cast<int>(em);
-  // a short depth is not split: adding the parts would cost more than it saves
-  const int64_t per = (dc + sms - 1) / sms;
-  p.dc_per = static_cast<int>(tk <= kPrShort ? (per + tk - 1) / (tk ? tk : 1) * tk : per);
-  p.dc_ctas = p.dc_per ? static_cast<int>((dc + p.dc_per - 1) / p.dc_per) : 0;
+  plan_dc(p, sms, em * nt, tk);
+  p.fits = du < (1ll << 31) && p.fits;
   auto bytes = [](int64_t a, int64_t b, int64_t c) { return (static_cast<size_t>(a) * b * c + 255) / 256 * 256; };
   p.half_du = T > kHalfAbove;
   p.bf16 = bytes(T, E, 3 * 2);
@@ -854,6 +883,11 @@ extern "C" moe_status moe_route_backward(
       return MOE_ERR_CUDA;
     if (plan.dc_per % plan.dc_kb != 0)  // else every CTA's tiles are whole
       left = Parts{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
+    if (left.tiles && !(du && plan.du_ctas >= kPrAdders && (plan.dc_kb - 1) / plan.dc_per + 2 <= kPrAdds + 1)) {
+      const int64_t groups = static_cast<int64_t>(left.tiles) * (kPrM / 4);
+      if (!launch(reduce_kernel, std::min<int64_t>(groups, 8 * moe_num_sms()), 64, 0, true, st, left)) return MOE_ERR_CUDA;
+      left = Parts{};
+    }
   }
   if (du) {
     const uint32_t n = half_du ? 2 : 3;
@@ -870,10 +904,6 @@ extern "C" moe_status moe_route_backward(
         ? launch(product_kernel<false, 2>, plan.du_ctas, kPrThreads, Ring<false, 2>::kSmem, true, st, a, b, in, out, out, args)
         : launch(product_kernel<false, 3>, plan.du_ctas, kPrThreads, Ring<false, 3>::kSmem, true, st, a, b, in, out, out, args);
     if (!ok) return MOE_ERR_CUDA;
-  } else if (left.tiles) {
-    const int groups = left.tiles * (kPrM / 4);
-    reduce_kernel<<<std::min(groups, 8 * moe_num_sms()), 64, 0, st>>>(left);
-    MOE_CUDA_CHECK_LAUNCH();
   }
   return MOE_OK;
 }
