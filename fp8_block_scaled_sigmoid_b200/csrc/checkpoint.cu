@@ -7,11 +7,16 @@
 //   moe_combine_checkpoint           out = u + Ys + sum_k gate_k Y[r_k];  yq, ys = Q(Y[r_k])
 //   moe_combine_checkpoint_backward  dy[r_k] = Q2(gate_k dout);  dgate_k = dout . (yq ys)[r_k]
 //
-// Both are HBM-bound streaming kernels, one CTA per token.  A warp takes four
-// 128-column tiles at a time, eight lanes a tile: lane l of a tile holds the
-// columns 32 s + 4 l .. + 3 (s = 0..3), so that every fp32 access is a
-// coalesced 16-byte one and a tile's maximum takes three shuffles for 16
-// values a lane (one lane per 4 values would take five).
+// Both are streaming kernels.  A warp takes four 128-column tiles of a token at a
+// time through all of its K rows, eight lanes a tile: lane l of a tile holds the
+// columns 32 s + 4 l .. + 3 (s = 0..3), so that every fp32 access is a coalesced
+// 16-byte one and a tile's maximum takes three shuffles for 16 values a lane
+// (one lane per 4 values would take five).  The forward's pieces are CTAs' warps
+// in any order; the backward's share a CTA a token, for the sums of dgate.
+// One B200, 4096 tokens x 8 experts x 7168: the combine with its checkpoint 238
+// us, 96% of the measured copy rate (HBM bound); its backward 123 us, 80% (half
+// its issue slots go to the conversions and scales of the K + 1 rows), 300 us
+// with the fp32 rows as well.
 #include <cuda_fp8.h>
 
 #include "epi_math.cuh"

@@ -39,7 +39,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // The three kernels of a call are launched to overlap: the next one's CTAs come
 // in (and set up their barriers and TMEM) as this one's leave, and wait for its
-// results where they need them.
+// results where they need them (and read them past L1).
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int e = 128 * i + 4 * lane;
-    const float4 c = e < E ? *reinterpret_cast<const float4*>(terms.cent_inv + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 c = e < E ? __ldcg(reinterpret_cast<const float4*>(terms.cent_inv + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
     out[4 * i] = __fmul_rn(out[4 * i], c.x);
     out[4 * i + 1] = __fmul_rn(out[4 * i + 1], c.y);
     out[4 * i + 2] = __fmul_rn(out[4 * i + 2], c.z);
@@ -260,8 +260,9 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 }
 
 // ------------------------------------------------------------- products --
-// D [M][N] = (base) + A [M][L] B [L][N] with A the three bf16 terms of dz and
-// B bf16, N contiguous (the tensor core reads it as an MN-major operand).
+// D [M][N] = (base) + A [M][L] B [L][N] with A the terms of dz (TERMS: three in
+// bf16, two in half) and B of the same type, N contiguous (the tensor core reads
+// it as an MN-major operand).
 //   du: A = dz as stored (M = tokens, depth = experts), B = the centroids
 //   dC: A = dz transposed, also MN-major (M = experts, depth = tokens), B = u
 // Tiles of 128 x 256 over depth blocks of 32.  One thread issues the TMA
@@ -341,8 +342,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint3
   return d;
 }
 
-// TMA store of a patch, and the wait for all but the last N stores to have
-// read (or, Done, written) theirs.
+// TMA store of a patch; the waits: for all but the last N stores to have read
+// theirs, and for all to have written.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t c0,
                                              int32_t c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -405,7 +406,7 @@ __device__ __forceinline__ void add_parts(const Parts& a, int worker, int worker
         const int slot = 2 * (c + i) + ((c + i) * a.per / a.KB == tile ? 0 : 1);
         const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot) * kPrM + r0) * kPrN) + thread;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) v[i][r] = c + i <= c1 ? __ldg(p + r * (kPrN / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < ROWS; ++r) v[i][r] = c + i <= c1 ? __ldcg(p + r * (kPrN / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i)
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       pos += g.k1 - g.k0;
       // the row's power of two back
       float row_scale = 1.f;
-      if (TERMS == 2 && g.m0 + quarter * 32 + lane < args.M) row_scale = __ldg(args.row_scale + g.m0 + quarter * 32 + lane);
+      if (TERMS == 2 && g.m0 + quarter * 32 + lane < args.M) row_scale = __ldcg(args.row_scale + g.m0 + quarter * 32 + lane);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -693,7 +694,9 @@ bool launch(void (*kern)(P...), int64_t grid, int block, int smem, bool behind, 
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 // Tokens above which du takes half operands: the call takes 567 us against 628

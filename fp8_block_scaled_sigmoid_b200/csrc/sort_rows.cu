@@ -12,7 +12,12 @@
 // is read once and written once, with a few fp32 operations an element.  A
 // warp takes one stretch of a token's columns through all of its K rows, eight
 // accesses a lane at a time: the loads of several sorted rows are in flight
-// together, and the token's values stay in registers.
+// together, and the token's values stay in registers as the words they were read
+// as (as separate 16-bit elements they cost twice the registers, and with them
+// half the warps that hide the latency).
+// One B200, rows of 7168 in bf16, of the measured copy rate of 6.44 TB/s:
+//   sort            4096 tokens x 8: 87 us, 95%     its backward:    83 us, 99%
+//   unsort backward 16384 x 6:      474 us, 100%    one token's sort: 1.8 us
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,8 +31,10 @@ constexpr int kSrWarps = 4;      // warps of a CTA, each with a piece of its own
 constexpr int kSrDotWarps = 16;  // most warps of a CTA whose warps share a token
 constexpr int kSrFlight = 8;     // accesses a lane has in flight: U columns x kSrFlight / U rows
 
+// Columns and rows a lane of the dot kernel has in flight: fewer than elsewhere,
+// so that 32 warps an SM fit (16384 x 6: 474 us; four columns 597).
 template <int N>
-constexpr int kSrDotU = N <= 2 ? 4 : 2;  // columns and rows in flight there
+constexpr int kSrDotU = N <= 2 ? 4 : 2;
 constexpr int kSrDotB = 2;
 
 // N elements of T as one access of plain words (16 bytes, or where the rows'
@@ -143,8 +150,8 @@ __device__ __forceinline__ void read_rows(Raw (&v)[B][U], const void* base, int6
   }
 }
 
-// blockDim = (32 * warps of a token, tokens).  dst row = round(w * src) (the
-// row itself without weights).
+// dst row = round(w * src) (the row itself, bit for bit, without weights).  A
+// CTA's warps have a piece of some token's columns each, whatever the token.
 template <typename T, int N, int U, bool WEIGHTED>
 __global__ void __launch_bounds__(32 * kSrWarps) scatter_rows_kernel(
     const T* __restrict__ src, int64_t lds, const int32_t* __restrict__ dst_of,
