@@ -833,7 +833,7 @@ extern "C" moe_status moe_route_backward(
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(u) || !aligned16(centroids) || ldu % 8 != 0 ||
       !aligned16(du_base) || !aligned16(du) || !aligned16(dcentroids) || !aligned16(dlogits) ||
-      !aligned4(dgate) || !aligned4(topk_idx) || !aligned4(topk_gate) || !aligned4(f) || !aligned4(dloss))
+      !aligned16(f) || !aligned4(dgate) || !aligned4(topk_idx) || !aligned4(topk_gate) || !aligned4(dloss))
     return MOE_ERR_ALIGN;
   size_t need = 0;
   if (moe_route_backward_workspace_size(T, d, E, &need) != MOE_OK) return MOE_ERR_UNSUPPORTED;

@@ -64,7 +64,7 @@ def route(L, dg=16, z=16, idx=16, gate=16, u=16, ldu=128, cent=16, T=8, d=128, E
     (route, dict(cent=None), 1), (route, dict(u=None), 1), (route, dict(f=16, S=0), 1),
     (route, dict(E=24), 2), (route, dict(d=192), 2), (route, dict(K=17), 2), (route, dict(ldu=64), 2),
     (route, dict(f=16, S=3), 2), (route, dict(E=2048), 4), (route, dict(E=64, K=33), 4),
-    (route, dict(z=20), 3), (route, dict(ldu=132), 3), (route, dict(du=20), 3), (route, dict(dg=18), 3),
+    (route, dict(z=20), 3), (route, dict(ldu=132), 3), (route, dict(du=20), 3), (route, dict(f=20, S=4), 3), (route, dict(dg=18), 3),
     (route, dict(nws=0), 6), (route, dict(ws=None), 6), (route, dict(ws=20), 3),
 ])
 def test_refused_on_the_host(call, kw, code):
