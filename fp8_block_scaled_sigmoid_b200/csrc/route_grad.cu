@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
     if (mine < 0 || mine >= E) {
       set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
       mine = -1;
-      g = 0.f;
+      g = a = 0.f;  // whatever dgate holds there
     }
   }
   // s and 1 - s from one exponential: e^-|z| / (1 + e^-|z|) and 1 / (1 + e^-|z|)

@@ -193,6 +193,31 @@ def test_bad_index_is_reported(cuda_dev):
     assert int(err.item()) == 3 and bool(torch.isfinite(dl).all())
 
 
+def test_bad_index_leaves_the_rest_alone(cuda_dev):
+    """A pair with a bad index is left out whatever its gradient holds."""
+    c = _case(9, 32, 128, 4, 0, 21, cuda_dev)
+    want = _call(dict(c, gate=c["gate"].clone().index_put_((torch.tensor([4]), torch.tensor([2])), torch.zeros(1, device=cuda_dev))), 0)
+    c["idx"][4, 2] = 77
+    for v in (float("nan"), float("inf")):
+        c["dgate"][4, 2] = v
+        err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+        got = _call(c, 0, dev_err=err)
+        assert int(err.item()) == 3
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T,E,K", [(1, 16, 2), (33, 48, 6), (70, 256, 32)])
+def test_the_same_expert_twice(cuda_dev, T, E, K):
+    """Pairs of one token that name the same expert add up."""
+    c = _case(T, E, 256, K, 0, 23 + T, cuda_dev)
+    c["idx"][:, 1] = c["idx"][:, 0]
+    if K > 4:
+        c["idx"][::2, 2:5] = c["idx"][::2, 5:6]
+    out = _call(c, 0)
+    _check(c, 0, out)
+    assert all(torch.equal(a, b) for a, b in zip(out, _call(c, 0)))
+
+
 def test_strided_tokens(cuda_dev):
     c = _case(50, 32, 256, 4, 0, 13, cuda_dev)
     want = _call(c, 0)
