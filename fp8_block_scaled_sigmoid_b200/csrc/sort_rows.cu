@@ -348,7 +348,7 @@ int access_bytes(uintptr_t bits, int e) { return bits % 16 == 0 ? 16 : (bits % 4
 moe_status check_shape(moe_dtype dt, int T, int K, int d, int64_t rows) {
   if (dt != MOE_BF16 && dt != MOE_F16 && dt != MOE_F32) return MOE_ERR_INVALID_ARG;
   if (T < 0 || K < 0 || d <= 0 || rows < 0) return MOE_ERR_INVALID_ARG;
-  if (K > kSrMaxK || rows > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
+  if (K > kSrMaxK || rows > 0x7FFFFFFFll || d > 1 << 30) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -505,7 +505,7 @@ moe_status moe_combine(const float* Y, const int32_t* dst_of, const float* topk_
  * result does not depend on timing.  No buffer written may overlap one read.
  * Pointers and leading dimensions need the element's own alignment only
  * (rows of whole 16-byte pieces, aligned to them, are fastest, 4-byte ones next).
- * Limits: d >= 1, 0 <= K <= 32, ld >= d, rows < 2^31.
+ * Limits: 1 <= d <= 2^30, 0 <= K <= 32, ld >= d, rows < 2^31.
  * =========================================================================== */
 
 /* moe_sort_rows -- xs[dst_of[t][k]] = x[t]. */

@@ -46,7 +46,7 @@ def route(L, dg=16, z=16, idx=16, gate=16, u=16, ldu=128, cent=16, T=8, d=128, E
     (sort, dict(x=None), 1), (sort, dict(xs=None), 1), (sort, dict(dst=None), 1),
     (sort, dict(ldx=63), 2), (sort, dict(ldxs=63), 2),
     (sort, dict(x=17), 3), (sort, dict(dt=F32, xs=18), 3), (sort, dict(dst=18), 3),
-    (sort, dict(K=33), 4), (sort, dict(rows=1 << 31), 4),
+    (sort, dict(K=33), 4), (sort, dict(d=(1 << 30) + 1, ldx=1 << 31, ldxs=1 << 31), 4), (sort, dict(rows=1 << 31), 4),
     (sort_bwd, dict(K=-1), 1), (sort_bwd, dict(g=None), 1), (sort_bwd, dict(dx=None), 1),
     (sort_bwd, dict(ldg=10), 2), (sort_bwd, dict(ldx=10), 2), (sort_bwd, dict(dx=17), 3), (sort_bwd, dict(K=40), 4),
     (unsort, dict(w=None), 1), (unsort, dict(dt=-1), 1), (unsort, dict(ldo=10), 2), (unsort, dict(w=18), 3),
