@@ -14,9 +14,10 @@
 //     of the product takes three MMAs.  Two terms would lose 2^-17 of a
 //     gradient, which the router keeps in high precision.  For many tokens du
 //     takes scaled half operands and two terms instead (half_centroids_kernel).
-//  3. The partial tiles of dC, whose depth T is split over the CTAs, are added
-//     in a fixed order, by two spare warps of du's CTAs while those work (or
-//     by reduce_kernel where du is not wanted).
+//     The two products run side by side, each on its share of the SMs
+//     (make_plan): du waits for memory while dC waits for the tensor cores.
+//  3. reduce_kernel -- where the depth T of dC's tiles is split over CTAs, their
+//     parts are added in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,8 +38,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The three kernels of a call are launched to overlap: the next one's CTAs come
-// in (and set up their barriers and TMEM) as this one's leave, and wait for its
+// The kernels of a call are launched to overlap: the next one's CTAs come in
+// (and set up their barriers and TMEM) as soon as there is room, and wait for
 // results where they need them (and read them past L1).
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -271,9 +272,8 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 // accumulators in registers: the two TMEM accumulators alternate every 128
 // deep, so that a tensor-core sum, whose additions may truncate, stays 24
 // steps long and the rest is rounded fp32 additions.  The depth blocks of all
-// tiles form one line that is cut evenly over the CTAs (for du at tile
-// borders): every SM gets the same work whatever the shape, and dC's few
-// tiles still fill the GPU.  An epilogue warp has 32 x 32 patches of its own in
+// tiles form one line that is cut over the CTAs as make_plan says, for du at
+// tile borders.  An epilogue warp has 32 x 32 patches of its own in
 // shared memory, which TMA fills with the base ahead of time and empties into
 // the result.
 // dC is bound by the tensor cores (16384 x 384 x 7168 in three terms: 190 us,
@@ -304,10 +304,6 @@ struct Ring {
   static constexpr int kSmem = 1024 + kStages * kStage + kPatches * kPrEpiWarps * kPrPatch + 512;
 };
 
-// CTAs of du from which its spare warps add dC's parts, and the most parts a
-// tile may have there (one thread adds them in turn).
-constexpr int kPrAdders = 100, kPrAdds = 4;
-
 // The parts of dC's tiles: CTA c worked on depth blocks [c * per, (c + 1) *
 // per) of the line; its part of its first tile is slot 2 c, of its last 2 c + 1.
 struct Parts {
@@ -321,10 +317,10 @@ struct ProductArgs {
   int mt;        // m tiles (the faster tile index)
   int units;     // depth blocks of all tiles
   int per;       // depth blocks of a CTA; 0: whole tiles, evenly
+  int first, share;  // whole tiles: the first CTAs take this many, the others the rest
   int has_base;
   int after_dc;  // du launched behind dC
   const float* row_scale;  // of half terms
-  Parts parts;   // du: dC's parts to add (tiles 0: none)
   int32_t* dev_err;
 };
 
@@ -386,43 +382,31 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
   a.w = __fadd_rn(a.w, b.w);
 }
 
-// Adds the parts of every tile that more than one CTA worked on, CTA by CTA;
-// 64 threads take ROWS rows of a tile at a time and read AHEAD parts ahead.
-template <int ROWS, int AHEAD>
-__device__ __forceinline__ void add_parts(const Parts& a, int worker, int workers, int thread) {
-  for (int g = worker; g < a.tiles * (kPrM / ROWS); g += workers) {
-    const int tile = g / (kPrM / ROWS), r0 = g % (kPrM / ROWS) * ROWS;
+// Adds the parts of every tile that more than one CTA worked on, CTA by CTA: a
+// CTA takes a row of a tile at a time and reads eight parts ahead.
+__global__ void __launch_bounds__(64) reduce_kernel(const Parts a) {
+  constexpr int kAhead = 8;
+  wait_predecessor();
+  for (int g = blockIdx.x; g < a.tiles * kPrM; g += gridDim.x) {
+    const int tile = g / kPrM, row = g % kPrM;
     const int c0 = tile * a.KB / a.per, c1 = ((tile + 1) * a.KB - 1) / a.per;
     if (c0 == c1) continue;
-    const int m = tile % a.mt * kPrM + r0, n = tile / a.mt * kPrN + 4 * thread;
-    if (m >= a.M || n >= a.N) continue;  // M is a multiple of ROWS
-    float4 sum[ROWS];
+    const int m = tile % a.mt * kPrM + row, n = tile / a.mt * kPrN + 4 * threadIdx.x;
+    if (m >= a.M || n >= a.N) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += kAhead) {
+      float4 v[kAhead];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) sum[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += AHEAD) {
-      float4 v[AHEAD][ROWS];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const int slot = 2 * (c + i) + ((c + i) * a.per / a.KB == tile ? 0 : 1);
-        const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot) * kPrM + r0) * kPrN) + thread;
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) v[i][r] = c + i <= c1 ? __ldcg(p + r * (kPrN / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot) * kPrM + row) * kPrN) + threadIdx.x;
+        v[i] = c + i <= c1 ? __ldcg(p) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) add4(sum[r], v[i][r]);
+      for (int i = 0; i < kAhead; ++i) add4(sum, v[i]);
     }
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-      *reinterpret_cast<float4*>(a.out + static_cast<int64_t>(m + r) * a.N + n) = sum[r];
+    *reinterpret_cast<float4*>(a.out + static_cast<int64_t>(m) * a.N + n) = sum;
   }
-}
-
-__global__ void __launch_bounds__(64) reduce_kernel(const Parts parts) {
-  wait_predecessor();
-  launch_dependents();
-  add_parts<1, 8>(parts, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 template <bool A_MN, int TERMS>
@@ -474,7 +458,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   volatile int* abort_v = abort_flag;
   // dC, and du without dC before it, need the terms that their predecessor
   // writes.  du after dC finds them complete, since dC lets it start only once
-  // it has them itself: only dC's parts have to be waited for.
+  // it has them itself; it runs beside dC and must only not end before it.
   if (!args.after_dc) wait_predecessor();
   if (A_MN) launch_dependents();
   int start, end;
@@ -483,8 +467,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
     end = min(args.units, start + args.per);
   } else {
     const int64_t tiles = args.units / args.KB;
-    start = static_cast<int>(tiles * blockIdx.x / gridDim.x) * args.KB;
-    end = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) * args.KB;
+    const bool early = static_cast<int>(blockIdx.x) < args.first;
+    const int64_t b = early ? blockIdx.x : blockIdx.x - args.first, n = early ? args.first : gridDim.x - args.first;
+    const int64_t t0 = early ? 0 : args.share, nt = early ? args.share : tiles - args.share;
+    start = static_cast<int>(t0 + nt * b / n) * args.KB;
+    end = static_cast<int>(t0 + nt * (b + 1) / n) * args.KB;
   }
 
   if (warp < 4) {
@@ -563,9 +550,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       }
       mma_commit(done);
       mbar_wait(done, 0, nullptr, args.dev_err);
-    } else if (!A_MN && warp >= 2) {
+    } else if (!A_MN && warp == 2) {
       if (args.after_dc) wait_predecessor();
-      if (args.parts.tiles) add_parts<4, 2>(args.parts, blockIdx.x, gridDim.x, threadIdx.x - 64);
     }
     __syncwarp();
   } else {
@@ -710,65 +696,110 @@ struct Plan {
   // scales of both, dC's parts
   size_t bf16, half, cent, cent_inv, row_scale, parts, all;
   bool half_du;
-  int du_units, du_kb, du_mt, du_ctas;
+  int du_units, du_kb, du_mt, du_ctas, du_first, du_share;
   int dc_units, dc_kb, dc_mt, dc_per, dc_ctas;
   bool fits;   // 32-bit arithmetic
 };
 
-// How dC's tiles, each tk depth blocks deep, are cut: whole, into n equal parts
-// (one CTA each, the depth padded with blocks of zeros), or evenly along the
-// line of all tiles (a CTA may then end one tile and begin the next).  A choice
-// costs, in depth blocks of about half a microsecond: the longest CTA's blocks,
-// 4 for each tile or part it writes, and for adding n parts up n / 4 and 4 in
-// du's spare warps, 12 in a kernel of its own.  920 tokens x 384 experts x 1024
-// take 28 us so and 58 with every line cut evenly, 200 x 384 x 1408 16 us with
-// whole tiles and 25 in seven parts.
-void plan_dc(Plan& p, int64_t sms, int64_t tiles, int64_t tk) {
-  auto adding = [&](int64_t n) { return (p.du_ctas >= kPrAdders && n <= kPrAdds ? 4 : 12) + n / 4; };
-  int64_t kb = tk, per = tk * ((tiles + sms - 1) / sms), best = per + 4;
-  for (int64_t n = 2; n <= 32 && n * tiles <= sms && n <= tk; ++n) {
-    const int64_t part = (tk + n - 1) / n, cost = part + 4 + adding(n);
-    if (cost < best) {
-      best = cost;
-      kb = part * n;
-      per = part;
+// How the products are cut, and which SMs they get.  dC's tiles, each tk depth
+// blocks deep, are taken whole (one, two, .. by a CTA), cut into n equal parts
+// (one CTA each, the depth padded with blocks of zeros), or cut evenly along the
+// line of all tiles over some number of CTAs (one may then end a tile and begin
+// the next).  du's CTAs have the other SMs from the start, with so many tiles each
+// that they end with those that get in when dC's CTAs leave.  Of all these the
+// one that ends first by the following times (in 10 ns, measured) is taken.
+// 4096 tokens x 256 experts x 7168 take 88 us so and 99 with each product on the
+// whole GPU in turn, 16384 x 384 397 and 436, 1024 x 256 31 and 39.
+constexpr int kDcBlock = 64, kDcPart = 250;     // a depth block; a tile's or a part's result
+constexpr int kDuTile = 150, kDuBlock3 = 85, kDuBlock2 = 57, kDuLeast = 600;  // a tile; HBM's share of it
+constexpr int kAdd = 800, kAddPart = 16;        // reduce_kernel; each part of a tile
+
+void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_t tk, int64_t du_tiles) {
+  const int64_t du_cost = std::max(kDuLeast, kDuTile + (p.half_du ? kDuBlock2 : kDuBlock3) * p.du_kb);
+  p.dc_kb = p.dc_per = p.dc_units = p.dc_ctas = p.du_first = p.du_share = 0;
+  p.du_ctas = static_cast<int>(std::min(sms, du_tiles));
+  p.fits = true;
+  if (!dc || tk == 0) return;
+  int64_t best = INT64_MAX;
+  // tiles of kb blocks, each CTA per blocks of the line, with so many results; parts of a tile
+  auto take = [&](int64_t kb, int64_t per, int64_t results, int64_t parts) {
+    const int64_t dc_end = per * kDcBlock + results * kDcPart, add = parts > 1 ? kAdd + kAddPart * parts : 0;
+    if (dc_end + add >= best) return;
+    const int64_t units = tiles * kb, ctas = (units + per - 1) / per, free = sms - ctas;
+    int64_t end = dc_end, first = 0, share = 0, on = 0;
+    if (du) {
+      // late tiles by each CTA that comes after dC's, early ones by the others
+      const int64_t ideal = (du_tiles * du_cost + ctas * dc_end) / sms;
+      const int64_t guess = std::max<int64_t>(0, (ideal - dc_end) / du_cost);
+      end = INT64_MAX;
+      for (int64_t late = guess; late <= guess + 1; ++late) {
+        const int64_t rest = std::max<int64_t>(0, du_tiles - late * ctas);
+        if (free == 0 && rest > 0) continue;
+        const int64_t early = free ? (rest + free - 1) / free : 0;
+        const int64_t e = std::max(early * du_cost, dc_end + late * du_cost);
+        if (e >= end) continue;
+        end = e;
+        first = rest == du_tiles ? 0 : std::min(free, rest);
+        share = first ? rest : 0;
+        on = first ? first + std::min(ctas, du_tiles - rest) : std::min(late ? ctas : free, du_tiles);
+      }
+      if (end == INT64_MAX) {  // no free SM, and more than a tile late
+        const int64_t late = (du_tiles + ctas - 1) / ctas;
+        end = dc_end + late * du_cost;
+        on = std::min(sms, du_tiles);
+      }
     }
+    if (end + add >= best) return;
+    best = end + add;
+    p.fits = units < (1ll << 31) && per < (1ll << 31);
+    p.dc_kb = static_cast<int>(kb);
+    p.dc_per = static_cast<int>(per);
+    p.dc_units = static_cast<int>(units);
+    p.dc_ctas = static_cast<int>(ctas);
+    if (!du) return;
+    p.du_ctas = static_cast<int>(on);
+    p.du_first = static_cast<int>(first);
+    p.du_share = static_cast<int>(share);
+  };
+  const int64_t least = (tiles + sms - 1) / sms;
+  for (int64_t m = least; m < least + 4; ++m) take(tk, tk * m, m, 1);
+  for (int64_t n = 2; n <= 32 && n * tiles <= sms && n <= tk; n += n < 4 ? 1 : n / 4) {
+    const int64_t part = (tk + n - 1) / n;
+    take(part * n, part, 1, n);
   }
-  const int64_t even = (tiles * tk + sms - 1) / sms;
-  if (even > 0 && even + 8 + adding(tk / even + 2) < best) {
-    kb = tk;
-    per = even;
+  auto even = [&](int64_t ctas) {
+    const int64_t per = ctas > 0 ? (tiles * tk + ctas - 1) / ctas : 0;
+    if (per > 0 && per % tk != 0) take(tk, per, per / tk + 2, tk / per + 2);
+  };
+  even(sms);
+  if (du) {
+    const int64_t work = tiles * tk * kDcBlock;
+    even(sms * work / (work + du_tiles * du_cost));
   }
-  const int64_t units = tiles * kb;
-  p.fits = units < (1ll << 31) && per < (1ll << 31);
-  p.dc_units = static_cast<int>(units);
-  p.dc_kb = static_cast<int>(kb);
-  p.dc_per = static_cast<int>(per);
-  p.dc_ctas = per ? static_cast<int>((units + per - 1) / per) : 0;
 }
 
-Plan make_plan(int T, int d, int E) {
+Plan make_plan(int T, int d, int E, bool du, bool dc) {
   Plan p;
   const int64_t sms = moe_num_sms();
   const int64_t nt = (d + kPrN - 1) / kPrN;
   const int64_t tm = (static_cast<int64_t>(T) + kPrM - 1) / kPrM, tk = (static_cast<int64_t>(T) + kPrK - 1) / kPrK;
   const int64_t em = (E + kPrM - 1) / kPrM, ek = (E + kPrK - 1) / kPrK;
-  const int64_t du = tm * nt * ek;
-  p.du_units = static_cast<int>(du);
+  const int64_t units = tm * nt * ek;
+  p.half_du = du && T > kHalfAbove;
+  p.du_units = static_cast<int>(units);
   p.du_kb = static_cast<int>(ek);
   p.du_mt = static_cast<int>(tm);
-  p.du_ctas = static_cast<int>(std::min(sms, tm * nt));
   p.dc_mt = static_cast<int>(em);
-  plan_dc(p, sms, em * nt, tk);
-  p.fits = du < (1ll << 31) && p.fits;
+  plan_products(p, du, dc, sms, em * nt, tk, tm * nt);
+  p.fits = units < (1ll << 31) && p.fits;
   auto bytes = [](int64_t a, int64_t b, int64_t c) { return (static_cast<size_t>(a) * b * c + 255) / 256 * 256; };
-  p.half_du = T > kHalfAbove;
-  p.bf16 = bytes(T, E, 3 * 2);
+  p.bf16 = dc || (du && !p.half_du) ? bytes(T, E, 3 * 2) : 0;
   p.half = p.half_du ? bytes(T, E, 2 * 2) : 0;
   p.cent = p.half_du ? bytes(E, d, 2) : 0;
   p.cent_inv = p.half_du ? bytes(E, 4, 1) : 0;
   p.row_scale = p.half_du ? bytes(T, 4, 1) : 0;
-  p.parts = static_cast<size_t>(2) * p.dc_ctas * kPrM * kPrN * sizeof(float);
+  const bool whole = p.dc_kb == 0 || p.dc_per % p.dc_kb == 0;
+  p.parts = whole ? 0 : static_cast<size_t>(2) * p.dc_ctas * kPrM * kPrN * sizeof(float);
   p.all = p.bf16 + p.half + p.cent + p.cent_inv + p.row_scale + p.parts;
   return p;
 }
@@ -805,9 +836,10 @@ extern "C" moe_status moe_route_backward_workspace_size(int T, int d, int E, siz
   if (!bytes) return MOE_ERR_INVALID_ARG;
   const moe_status s = moe::check_sizes(T, d, E);
   if (s != MOE_OK) return s;
-  const moe::Plan p = moe::make_plan(T, d, E);
-  if (!p.fits) return MOE_ERR_UNSUPPORTED;
-  *bytes = p.all;
+  // enough for a call with either or both products
+  const moe::Plan both = moe::make_plan(T, d, E, true, true), dc = moe::make_plan(T, d, E, false, true);
+  if (!both.fits || !dc.fits) return MOE_ERR_UNSUPPORTED;
+  *bytes = std::max(both.all, dc.all);
   return MOE_OK;
 }
 
@@ -835,12 +867,10 @@ extern "C" moe_status moe_route_backward(
       !aligned16(du_base) || !aligned16(du) || !aligned16(dcentroids) || !aligned16(dlogits) ||
       !aligned16(f) || !aligned4(dgate) || !aligned4(topk_idx) || !aligned4(topk_gate) || !aligned4(dloss))
     return MOE_ERR_ALIGN;
-  size_t need = 0;
-  if (moe_route_backward_workspace_size(T, d, E, &need) != MOE_OK) return MOE_ERR_UNSUPPORTED;
-  if (ws_bytes < need || !ws) return MOE_ERR_WORKSPACE;
-  if (!aligned16(ws)) return MOE_ERR_ALIGN;
-  const Plan plan = make_plan(T, d, E);
+  const Plan plan = make_plan(T, d, E, du, dcentroids);
   if (!plan.fits) return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < plan.all || !ws) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_ALIGN;
   uint8_t* at = static_cast<uint8_t*>(ws);
   auto take = [&](size_t n) {
     uint8_t* p = at;
@@ -853,7 +883,7 @@ extern "C" moe_status moe_route_backward(
   float* cent_inv = reinterpret_cast<float*>(take(plan.cent_inv));
   float* row_scale = reinterpret_cast<float*>(take(plan.row_scale));
   float* parts = reinterpret_cast<float*>(take(plan.parts));
-  const bool half_du = du && plan.half_du;
+  const bool half_du = plan.half_du;
   if ((du || dcentroids) && !grant_smem()) return MOE_ERR_CUDA;
   if (half_du && !launch(half_centroids_kernel, E, 256, 0, false, st, centroids, d, half_cent, cent_inv))
     return MOE_ERR_CUDA;
@@ -872,25 +902,18 @@ extern "C" moe_status moe_route_backward(
   const uint64_t rd = static_cast<uint64_t>(d) * 4, rz = static_cast<uint64_t>(E) * 2;
   const uint64_t stride[2] = {rz, rz * T};
   CUtensorMap a, b, in, out, part;
-  Parts left{};  // dC's parts that are still to be added
   if (dcentroids) {
     const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), 3};
     const uint32_t box[3] = {64, kPrK, 3};
     if (!moe_make_tmap_3d(&a, bf16_terms, bf16, extent, stride, box, 128) ||
         !moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
         !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
-        !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32))
+        (plan.parts && !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32)))
       return MOE_ERR_CUDA;
-    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, nullptr, Parts{}, dev_err};
+    if (!plan.parts) part = out;  // not used
+    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, 0, 0, nullptr, dev_err};
     if (!launch(product_kernel<true, 3>, plan.dc_ctas, kPrThreads, Ring<true, 3>::kSmem, true, st, a, b, out, out, part, args))
       return MOE_ERR_CUDA;
-    if (plan.dc_per % plan.dc_kb != 0)  // else every CTA's tiles are whole
-      left = Parts{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
-    if (left.tiles && !(du && plan.du_ctas >= kPrAdders && (plan.dc_kb - 1) / plan.dc_per + 2 <= kPrAdds + 1)) {
-      const int64_t groups = static_cast<int64_t>(left.tiles) * (kPrM / 4);
-      if (!launch(reduce_kernel, std::min<int64_t>(groups, 8 * moe_num_sms()), 64, 0, true, st, left)) return MOE_ERR_CUDA;
-      left = Parts{};
-    }
   }
   if (du) {
     const uint32_t n = half_du ? 2 : 3;
@@ -901,12 +924,17 @@ extern "C" moe_status moe_route_backward(
         !moe_make_tmap_2d(&in, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
         !moe_make_tmap_2d(&out, du, fp32, d, T, rd, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, du_base ? 1 : 0, dcentroids ? 1 : 0, row_scale,
-                           left, dev_err};
+    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, plan.du_first, plan.du_share,
+                           du_base ? 1 : 0, dcentroids ? 1 : 0, row_scale, dev_err};
     const bool ok = half_du
         ? launch(product_kernel<false, 2>, plan.du_ctas, kPrThreads, Ring<false, 2>::kSmem, true, st, a, b, in, out, out, args)
         : launch(product_kernel<false, 3>, plan.du_ctas, kPrThreads, Ring<false, 3>::kSmem, true, st, a, b, in, out, out, args);
     if (!ok) return MOE_ERR_CUDA;
+  }
+  if (plan.parts) {
+    const Parts left{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
+    const int64_t rows = static_cast<int64_t>(left.tiles) * kPrM;
+    if (!launch(reduce_kernel, std::min<int64_t>(rows, 16 * moe_num_sms()), 64, 0, true, st, left)) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
