@@ -304,12 +304,11 @@ struct Ring {
   static constexpr int kSmem = 1024 + kStages * kStage + kPatches * kPrEpiWarps * kPrPatch + 512;
 };
 
-// The parts of dC's tiles: CTA c worked on depth blocks [c * per, (c + 1) *
-// per) of the line; its part of its first tile is slot 2 c, of its last 2 c + 1.
+// The parts of dC's tiles, n of each: tile * n + i, [kPrM][kPrN] fp32.
 struct Parts {
   const float* part;
   float* out;
-  int tiles, KB, per, mt, M, N;
+  int tiles, n, mt, M, N;
 };
 
 struct ProductArgs {
@@ -359,11 +358,10 @@ __device__ __forceinline__ void tma_store_wait_done() {
 struct Segment {
   int m0, n0, k0, k1;
   bool whole;  // covers the tile's depth
-  bool first;  // the CTA's first tile
 };
 
 // The next stretch of one tile in [pos, end).
-__device__ __forceinline__ Segment next_segment(const ProductArgs& a, int start, int pos, int end) {
+__device__ __forceinline__ Segment next_segment(const ProductArgs& a, int pos, int end) {
   Segment s;
   const int tile = pos / a.KB;
   s.k0 = pos - tile * a.KB;
@@ -371,7 +369,6 @@ __device__ __forceinline__ Segment next_segment(const ProductArgs& a, int start,
   s.m0 = tile % a.mt * kPrM;
   s.n0 = tile / a.mt * kPrN;
   s.whole = s.k0 == 0 && s.k1 == a.KB;
-  s.first = pos == start;
   return s;
 }
 
@@ -382,28 +379,24 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
   a.w = __fadd_rn(a.w, b.w);
 }
 
-// Adds the parts of every tile that more than one CTA worked on, CTA by CTA: a
-// CTA takes a row of a tile at a time and reads eight parts ahead.
+// Adds the parts of every tile in turn: a CTA takes a row of a tile at a time
+// and reads eight parts ahead.
 __global__ void __launch_bounds__(64) reduce_kernel(const Parts a) {
   constexpr int kAhead = 8;
   wait_predecessor();
   for (int g = blockIdx.x; g < a.tiles * kPrM; g += gridDim.x) {
     const int tile = g / kPrM, row = g % kPrM;
-    const int c0 = tile * a.KB / a.per, c1 = ((tile + 1) * a.KB - 1) / a.per;
-    if (c0 == c1) continue;
     const int m = tile % a.mt * kPrM + row, n = tile / a.mt * kPrN + 4 * threadIdx.x;
     if (m >= a.M || n >= a.N) continue;
+    const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(tile) * a.n * kPrM + row) * kPrN) + threadIdx.x;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += kAhead) {
+    for (int i = 0; i < a.n; i += kAhead) {
       float4 v[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int slot = 2 * (c + i) + ((c + i) * a.per / a.KB == tile ? 0 : 1);
-        const float4* p = reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot) * kPrM + row) * kPrN) + threadIdx.x;
-        v[i] = c + i <= c1 ? __ldcg(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      for (int j = 0; j < kAhead; ++j)
+        v[j] = i + j < a.n ? __ldcg(p + static_cast<int64_t>(i + j) * (kPrM * kPrN / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) add4(sum, v[i]);
+      for (int j = 0; j < kAhead; ++j) add4(sum, v[j]);
     }
     *reinterpret_cast<float4*>(a.out + static_cast<int64_t>(m) * a.N + n) = sum;
   }
@@ -481,7 +474,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       int it = 0;
       bool live = true;
       for (int pos = start; pos < end && live;) {
-        const Segment g = next_segment(args, start, pos, end);
+        const Segment g = next_segment(args, pos, end);
         pos += g.k1 - g.k0;
         for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
           const int s = it % kStages;
@@ -515,7 +508,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       int it = 0, ch = 0;
       bool live = true;
       for (int pos = start; pos < end && live;) {
-        const Segment g = next_segment(args, start, pos, end);
+        const Segment g = next_segment(args, pos, end);
         pos += g.k1 - g.k0;
         for (int kc = g.k0; kc < g.k1 && live; kc += kPrChunk, ++ch) {
           const int p = ch & 1;
@@ -587,7 +580,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
     int ch = 0;
     bool ok = true;
     for (int pos = start; pos < end && ok;) {
-      const Segment g = next_segment(args, start, pos, end);
+      const Segment g = next_segment(args, pos, end);
       pos += g.k1 - g.k0;
       // the row's power of two back
       float row_scale = 1.f;
@@ -613,12 +606,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
         if (lane == 0) mbar_arrive(&acc_empty[p]);
       }
       if (!ok) break;
-      // whole tiles go to the result, a part of a tile to the CTA's slot of
-      // its first or its last tile
+      // whole tiles go to the result, the part of one to the CTA's place
       const bool direct = !A_MN || g.whole;
       if (direct && (g.n0 + half * 128 >= args.N || g.m0 + quarter * 32 >= args.M)) continue;
       const CUtensorMap* dst = direct ? &tmOut : &tmPart;
-      const int row0 = direct ? g.m0 + quarter * 32 : (2 * static_cast<int>(blockIdx.x) + (g.first ? 0 : 1)) * kPrM + quarter * 32;
+      const int row0 = direct ? g.m0 + quarter * 32 : static_cast<int>(blockIdx.x) * kPrM + quarter * 32;
       const int col0 = direct ? g.n0 + half * 128 : half * 128;
 #pragma unroll
       for (int b = 0; b < 4; ++b, ++used) {
@@ -702,17 +694,16 @@ struct Plan {
 };
 
 // How the products are cut, and which SMs they get.  dC's tiles, each tk depth
-// blocks deep, are taken whole (one, two, .. by a CTA), cut into n equal parts
-// (one CTA each, the depth padded with blocks of zeros), or cut evenly along the
-// line of all tiles over some number of CTAs (one may then end a tile and begin
-// the next).  du's CTAs have the other SMs from the start, with so many tiles each
-// that they end with those that get in when dC's CTAs leave.  Of all these the
-// one that ends first by the following times (in 10 ns, measured) is taken.
+// blocks deep, are taken whole (one, two, .. by a CTA) or cut into n equal parts
+// (one CTA each, the depth padded with blocks of zeros).  du's CTAs have the
+// other SMs from the start, with so many tiles each that they end with those that
+// get in when dC's CTAs leave.  Of all these the one that ends first by the
+// following times (in 10 ns, measured) is taken.
 // 4096 tokens x 256 experts x 7168 take 88 us so and 99 with each product on the
 // whole GPU in turn, 16384 x 384 397 and 436, 1024 x 256 31 and 39.
 constexpr int kDcBlock = 64, kDcPart = 250;     // a depth block; a tile's or a part's result
 constexpr int kDuTile = 150, kDuBlock3 = 85, kDuBlock2 = 57, kDuLeast = 600;  // a tile; HBM's share of it
-constexpr int kAdd = 800, kAddPart = 16;        // reduce_kernel; each part of a tile
+constexpr int kAdd = 500, kAddPart = 16;        // reduce_kernel; each part of a tile
 
 void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_t tk, int64_t du_tiles) {
   const int64_t du_cost = std::max(kDuLeast, kDuTile + (p.half_du ? kDuBlock2 : kDuBlock3) * p.du_kb);
@@ -721,9 +712,10 @@ void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_
   p.fits = true;
   if (!dc || tk == 0) return;
   int64_t best = INT64_MAX;
-  // tiles of kb blocks, each CTA per blocks of the line, with so many results; parts of a tile
-  auto take = [&](int64_t kb, int64_t per, int64_t results, int64_t parts) {
-    const int64_t dc_end = per * kDcBlock + results * kDcPart, add = parts > 1 ? kAdd + kAddPart * parts : 0;
+  // tiles of kb blocks (padded), per blocks of their line a CTA, each tile in so many parts
+  auto take = [&](int64_t kb, int64_t per, int64_t parts) {
+    const int64_t dc_end = per * kDcBlock + (parts > 1 ? 1 : per / kb) * kDcPart;
+    const int64_t add = parts > 1 ? kAdd + kAddPart * parts : 0;
     if (dc_end + add >= best) return;
     const int64_t units = tiles * kb, ctas = (units + per - 1) / per, free = sms - ctas;
     int64_t end = dc_end, first = 0, share = 0, on = 0;
@@ -762,19 +754,10 @@ void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_
     p.du_share = static_cast<int>(share);
   };
   const int64_t least = (tiles + sms - 1) / sms;
-  for (int64_t m = least; m < least + 4; ++m) take(tk, tk * m, m, 1);
+  for (int64_t m = least; m < least + 4; ++m) take(tk, tk * m, 1);
   for (int64_t n = 2; n <= 32 && n * tiles <= sms && n <= tk; n += n < 4 ? 1 : n / 4) {
     const int64_t part = (tk + n - 1) / n;
-    take(part * n, part, 1, n);
-  }
-  auto even = [&](int64_t ctas) {
-    const int64_t per = ctas > 0 ? (tiles * tk + ctas - 1) / ctas : 0;
-    if (per > 0 && per % tk != 0) take(tk, per, per / tk + 2, tk / per + 2);
-  };
-  even(sms);
-  if (du) {
-    const int64_t work = tiles * tk * kDcBlock;
-    even(sms * work / (work + du_tiles * du_cost));
+    take(part * n, part, n);
   }
 }
 
@@ -798,8 +781,7 @@ Plan make_plan(int T, int d, int E, bool du, bool dc) {
   p.cent = p.half_du ? bytes(E, d, 2) : 0;
   p.cent_inv = p.half_du ? bytes(E, 4, 1) : 0;
   p.row_scale = p.half_du ? bytes(T, 4, 1) : 0;
-  const bool whole = p.dc_kb == 0 || p.dc_per % p.dc_kb == 0;
-  p.parts = whole ? 0 : static_cast<size_t>(2) * p.dc_ctas * kPrM * kPrN * sizeof(float);
+  p.parts = p.dc_per < p.dc_kb ? static_cast<size_t>(p.dc_ctas) * kPrM * kPrN * sizeof(float) : 0;
   p.all = p.bf16 + p.half + p.cent + p.cent_inv + p.row_scale + p.parts;
   return p;
 }
@@ -908,7 +890,7 @@ extern "C" moe_status moe_route_backward(
     if (!moe_make_tmap_3d(&a, bf16_terms, bf16, extent, stride, box, 128) ||
         !moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
         !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
-        (plan.parts && !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(2) * plan.dc_ctas * kPrM, kPrN * 4, 32, 32)))
+        (plan.parts && !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(plan.dc_ctas) * kPrM, kPrN * 4, 32, 32)))
       return MOE_ERR_CUDA;
     if (!plan.parts) part = out;  // not used
     const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, 0, 0, nullptr, dev_err};
@@ -932,9 +914,9 @@ extern "C" moe_status moe_route_backward(
     if (!ok) return MOE_ERR_CUDA;
   }
   if (plan.parts) {
-    const Parts left{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb, plan.dc_per, plan.dc_mt, E, d};
-    const int64_t rows = static_cast<int64_t>(left.tiles) * kPrM;
-    if (!launch(reduce_kernel, std::min<int64_t>(rows, 16 * moe_num_sms()), 64, 0, true, st, left)) return MOE_ERR_CUDA;
+    const Parts all{parts, dcentroids, plan.dc_units / plan.dc_kb, plan.dc_kb / plan.dc_per, plan.dc_mt, E, d};
+    const int64_t rows = static_cast<int64_t>(all.tiles) * kPrM;
+    if (!launch(reduce_kernel, std::min<int64_t>(rows, 16 * moe_num_sms()), 64, 0, true, st, all)) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }

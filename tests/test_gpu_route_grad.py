@@ -84,8 +84,9 @@ CASES = [
     (1, 16, 128, 1, 0), (1, 256, 7168, 8, 1), (37, 16, 256, 4, 0), (129, 80, 384, 6, 3), (128, 48, 640, 16, 4),
     (200, 256, 7168, 8, 0), (300, 384, 1152, 6, 2), (257, 1024, 256, 32, 1), (1000, 128, 2048, 2, 8),
     (2500, 272, 896, 8, 5), (4097, 64, 512, 4, 0), (4608, 272, 384, 8, 4),
-    # dC's tiles in many equal parts, in two, cut along the line
+    # dC's tiles in many equal parts, whole, two to a CTA; du in CTAs beside dC's and behind them
     (920, 384, 1024, 8, 1), (3000, 16, 128, 2, 0), (1024, 256, 7168, 8, 4), (1100, 1024, 5376, 4, 0),
+    (2100, 512, 2048, 8, 0), (300, 384, 7168, 6, 1), (6000, 128, 2048, 8, 2),
 ]
 
 
