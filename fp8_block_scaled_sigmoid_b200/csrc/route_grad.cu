@@ -276,12 +276,11 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
 // tile borders.  An epilogue warp has 32 x 32 patches of its own in
 // shared memory, which TMA fills with the base ahead of time and empties into
 // the result.
-// dC is bound by the tensor cores (16384 x 384 x 7168 in three terms: 190 us,
-// 1.42 PFLOP/s with the power cap holding the clock near 1.5 GHz).  du reads the
-// base and writes du besides (4096 x 7168 fp32: 36 us at the copy rate) and
-// takes 58 us there: its operand loads wait behind those streams; deeper
-// patches, contiguous operands, narrower tiles, L2 prefetches and pairs of CTAs
-// (cta_group::2) were all tried and gave nothing more.
+// A depth block of dC takes a CTA 0.64 us, 87% of the measured tensor peak.  du
+// reads the base and writes du besides (4096 x 7168 fp32: 36 us at the copy rate)
+// and takes 58 us there on the whole GPU: its operand loads wait behind those
+// streams; deeper patches, contiguous operands, narrower tiles, L2 prefetches and
+// pairs of CTAs (cta_group::2) gave nothing more, dC at its side did.
 constexpr uint32_t kFmtF16 = 0;  // kind::f16
 constexpr int kPrM = 128, kPrN = 256, kPrK = 32;
 constexpr int kPrChunk = 4;                       // depth blocks per accumulator
@@ -677,11 +676,12 @@ bool launch(void (*kern)(P...), int64_t grid, int block, int smem, bool behind, 
   return false;
 }
 
-// Tokens above which du takes half operands: the call takes 567 us against 628
-// at 16384 tokens and 384 experts, the same at 4096 (118 against 119) and more
-// below (50 against 43 at 1024), where converting the centroids costs what the
-// product saves.
-constexpr int kHalfAbove = 4096;
+// Tokens and experts above which du takes half operands: the call takes 412 us
+// against 437 so at 16384 tokens x 384 experts x 7168, 154 against 165 at 6000,
+// but 114 against 116 at 4096 and 96 against 88 there with 256 experts, where
+// converting the centroids first costs what the product saves.  With few experts
+// du waits for memory either way (16384 x 128 x 4096: 151 against 149).
+constexpr int kHalfAbove = 4096, kHalfExperts = 128;
 
 struct Plan {
   // workspace bytes: dz in bf16 and in half terms, the centroids in half, the
@@ -700,7 +700,8 @@ struct Plan {
 // get in when dC's CTAs leave.  Of all these the one that ends first by the
 // following times (in 10 ns, measured) is taken.
 // 4096 tokens x 256 experts x 7168 take 88 us so and 99 with each product on the
-// whole GPU in turn, 16384 x 384 397 and 436, 1024 x 256 31 and 39.
+// whole GPU in turn, 16384 x 384 412 and 437, 1024 x 256 31 and 39, 6000 x 64 x
+// 2048 36 and 72.
 constexpr int kDcBlock = 64, kDcPart = 250;     // a depth block; a tile's or a part's result
 constexpr int kDuTile = 150, kDuBlock3 = 85, kDuBlock2 = 57, kDuLeast = 600;  // a tile; HBM's share of it
 constexpr int kAdd = 500, kAddPart = 16;        // reduce_kernel; each part of a tile
@@ -768,7 +769,7 @@ Plan make_plan(int T, int d, int E, bool du, bool dc) {
   const int64_t tm = (static_cast<int64_t>(T) + kPrM - 1) / kPrM, tk = (static_cast<int64_t>(T) + kPrK - 1) / kPrK;
   const int64_t em = (E + kPrM - 1) / kPrM, ek = (E + kPrK - 1) / kPrK;
   const int64_t units = tm * nt * ek;
-  p.half_du = du && T > kHalfAbove;
+  p.half_du = du && T > kHalfAbove && E > kHalfExperts;
   p.du_units = static_cast<int>(units);
   p.du_kb = static_cast<int>(ek);
   p.du_mt = static_cast<int>(tm);

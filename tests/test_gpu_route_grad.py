@@ -121,14 +121,15 @@ def test_extreme_logits(cuda_dev):
     _check(c, 2, out)
 
 
-def test_many_tokens_with_uneven_scales(cuda_dev):
-    """Above 4096 tokens du is the product of scaled half operands: centroids
+@pytest.mark.parametrize("E", [48, 144])
+def test_many_tokens_with_uneven_scales(cuda_dev, E):
+    """Above 4096 tokens and 128 experts du is the product of scaled half operands: centroids
     and gradient rows of very different sizes, zero ones among them.  Two half
     terms hold dz within 2^-23 of a value and 2^-39 of its row's largest
     contribution top = max_e |dz_e| max|C_e| (half's smallest step is 2^-24,
     the row's largest value at least 2^14), a half centroid within 2^-39 of
     its largest element."""
-    T, E, d, K = 4100, 48, 384, 4
+    T, d, K = 4100, 384, 4
     c = _case(T, E, d, K, 4, 17, cuda_dev)
     c["cent"][3] = 0.0
     c["cent"][5] *= 2.0 ** 30
