@@ -14,9 +14,8 @@
 // (one lane per 4 values would take five).  The forward's pieces are CTAs' warps
 // in any order; the backward's share a CTA a token, for the sums of dgate.
 // One B200, 4096 tokens x 8 experts x 7168: the combine with its checkpoint 238
-// us, 96% of the measured copy rate (HBM bound); its backward 123 us, 80% (half
-// its issue slots go to the conversions and scales of the K + 1 rows), 300 us
-// with the fp32 rows as well.
+// us, 96% of the measured copy rate (HBM bound); its backward 109 us, 90%, and 285
+// us, 92%, with the fp32 rows as well.
 #include <cuda_fp8.h>
 
 #include "epi_math.cuh"
@@ -37,9 +36,9 @@ struct Shape {
 };
 
 // Four warps a token where that gives an SM 24 warps, more where the tokens are
-// few, up to 16 (x 8 experts x 7168: 256 tokens 10.5 us against 14.2 with four,
-// 1024 tokens 38 with four against 46 with five); several tokens a CTA where a
-// token has fewer pieces.
+// few, up to 16 (x 8 experts x 7168: 200 tokens 8.9 us with 14 against 9.7 with
+// seven, 700 tokens 20.8 with five against 22.6 with four); several tokens a CTA
+// where a token has fewer pieces.
 Shape ck_shape(int T, int K, int tiles) {
   const int items = (tiles + kCkTiles - 1) / kCkTiles;
   const int64_t want = (static_cast<int64_t>(moe_num_sms()) * 24 + T - 1) / T;
@@ -48,7 +47,7 @@ Shape ck_shape(int T, int K, int tiles) {
   const int warps = (items + steps - 1) / steps;
   const int tokens = warps >= kCkWarps ? 1 : kCkWarps / warps;
   return {dim3(32 * warps, tokens), static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens),
-          static_cast<size_t>(tokens) * warps * K * 8 * sizeof(float)};
+          static_cast<size_t>(tokens) * warps * (K * 8 + 256) * sizeof(float)};
 }
 
 // Two E4M3 bytes -> two floats (exact: every E4M3 value is a half value).
@@ -192,76 +191,102 @@ __global__ void __launch_bounds__(32 * kCkWarps) combine_checkpoint_kernel(
   }
 }
 
-// dout is read once a tile and gives all K + 1 gradient tiles.  Its largest
-// magnitude is found once: rounding is monotone, so the largest |fl(g x)| is
-// fl(|g| max |x|).  Power-of-two scales divide exactly: a product with the
-// inverse gives the quotient, and folded into the gate it gives the same
-// bits with one product (a gate beyond 1e30 keeps the two).  Without dy a lane
-// holds 16 neighbouring columns, so that a row's codes are one 16-byte access
-// a lane; with it the columns 32 s + 4 l, so that the fp32 rows' are.
-// At most WARPS warps a CTA; with four, 40 warps an SM (48 registers a thread)
-// beat 28 with 64: 123 us against 131 for 4096 x 8 rows of 7168.
-template <bool WITH_DY, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == kCkWarps ? 10 : 2) combine_checkpoint_backward_kernel(
+// dout is read once a tile (and ROWS experts) and gives all gradient tiles.  Its
+// largest magnitude is found once: rounding is monotone, so the largest |fl(g x)| is
+// fl(|g| max |x|).  The 32 scales of four tiles and eight experts are computed by
+// the 32 lanes at once and handed out by shuffles.  Power-of-two scales divide
+// exactly: a product with the inverse gives the quotient, and folded into the gate
+// it gives the same bits with one product (a gate beyond 1e30 keeps the two).
+// Without dy a lane holds 16 neighbouring columns, so that a row's codes are one
+// 16-byte access a lane; with it the columns 32 s + 4 l, so that the fp32 rows' are.
+// What counts besides is that the codes are asked for three rows ahead: without
+// the conversions the kernel took as long, one row ahead with 40 warps an SM took
+// 123 us for 4096 x 8 rows of 7168, three ahead with 28 (72 registers a thread)
+// takes 109.  ROWS is 8, 4 or 2 by K, with more than 8 in turns of 8 (lane l
+// has expert l % 8 of a turn, so fewer ROWS are for K <= ROWS alone); 4096 x 4
+// rows take 67 us with four and 70 with eight, 4096 x 2 of 5120 35 with two
+// and 42.  At most WARPS warps a CTA.
+template <bool WITH_DY, int WARPS, int ROWS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS > kCkWarps ? 2 : (ROWS == 2 ? 8 : 7)) combine_checkpoint_backward_kernel(
     const float* __restrict__ dout, const int32_t* __restrict__ dst_of,
     const float* __restrict__ gate, const uint8_t* __restrict__ yq, const float* __restrict__ ys,
     int64_t rows, int T, int K, int d, uint8_t* __restrict__ dyq, float* __restrict__ dys,
     float* __restrict__ dy, float* __restrict__ dgate, int32_t* dev_err) {
-  extern __shared__ float dot[];  // [tokens][warps][K][8]
+  extern __shared__ float dot[];  // [tokens][warps][K][8], then [tokens][warps][8][32]
   constexpr int kLane = WITH_DY ? 4 : 16, kStep = WITH_DY ? 32 : 4;
+  constexpr int kAhead = ROWS < 3 ? ROWS : 3;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t P = static_cast<int64_t>(T) * K;
   int row;
   float g;
   load_pair(dst_of, gate, t, K, lane, rows < P ? rows : P, t < T, row, g, dev_err);
-  const uint32_t kept = __ballot_sync(0xffffffffu, row >= 0);
-  const int tiles = d / 128;
-  bool first = true;
-  for (int item = warp; item * kCkTiles < tiles && t < T; item += warps) {
-    const int j = item * kCkTiles + (lane >> 3);
-    const bool in = j < tiles;
-    const int64_t col = static_cast<int64_t>(j) * 128 + kLane * (lane & 7);
-    float4 a[4];
+  if (row < 0) g = 0.f;  // whatever a dropped pair's gate holds
+  const int tiles = d / 128, end = t < T ? tiles : 0;
+  float* mine = dot + blockDim.y * warps * K * 8 + (threadIdx.y * warps + warp) * 8 * 32 + lane;  // one lane's sums
+  int k0 = 0;
+  do {  // ROWS experts at a time (K == 0: the shared expert's rows alone)
+    const int my_row = __shfl_sync(0xffffffffu, row, k0 + (lane & 7));
+    const float my_gate = __shfl_sync(0xffffffffu, g, k0 + (lane & 7));
+    const bool plain = !WITH_DY && __all_sync(0xffffffffu, fabsf(my_gate) <= 1e30f);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      a[s] = in ? __ldg(reinterpret_cast<const float4*>(dout + t * d + col + kStep * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    float next_scale = 0.f;
-    auto fetch = [&](uint32_t left) {
-      const int r = __shfl_sync(0xffffffffu, row, __ffs(left) - 1);
-      if (!in) return;
-      const uint8_t* p = yq + static_cast<int64_t>(r) * d + col;
-      if (WITH_DY)
-        next = make_uint4(__ldg(reinterpret_cast<const uint32_t*>(p)), __ldg(reinterpret_cast<const uint32_t*>(p + 32)),
+    for (int m = 0; m < ROWS; ++m) mine[32 * m] = 0.f;
+    for (int item = warp; item * kCkTiles < end; item += warps) {
+      const int j = item * kCkTiles + (lane >> 3);
+      const bool in = j < tiles;
+      const int64_t col = static_cast<int64_t>(j) * 128 + kLane * (lane & 7);
+      float4 a[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        a[s] = in ? __ldg(reinterpret_cast<const float4*>(dout + t * d + col + kStep * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      uint4 next[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i] = make_uint4(0u, 0u, 0u, 0u);
+      auto fetch = [&](int m, uint4& to) {
+        const int r = __shfl_sync(0xffffffffu, row, k0 + m);
+        if (r < 0 || !in) return;
+        const uint8_t* p = yq + static_cast<int64_t>(r) * d + col;
+        if (WITH_DY)
+          to = make_uint4(__ldg(reinterpret_cast<const uint32_t*>(p)), __ldg(reinterpret_cast<const uint32_t*>(p + 32)),
                           __ldg(reinterpret_cast<const uint32_t*>(p + 64)), __ldg(reinterpret_cast<const uint32_t*>(p + 96)));
-      else
-        next = __ldg(reinterpret_cast<const uint4*>(p));
-      next_scale = __ldg(ys + static_cast<int64_t>(r) * tiles + j);
-    };
-    if (kept) fetch(kept);
-    const float amax = tile_amax(a);
-    uint64_t a2[8];
+        else
+          to = __ldg(reinterpret_cast<const uint4*>(p));
+      };
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      a2[2 * s] = pack2(a[s].x, a[s].y);
-      a2[2 * s + 1] = pack2(a[s].z, a[s].w);
-    }
-    auto write_row = [&](int64_t r, float w) {
-      const float scale = pow2_quant_scale(__fmul_rn(fabsf(w), amax));
+      for (int i = 0; i < kAhead; ++i) fetch(i, next[i]);
+      const int64_t my_tile = static_cast<int64_t>(my_row) * tiles + j;
+      const float my_ys = my_row >= 0 && in ? __ldg(ys + my_tile) : 0.f;
+      const float amax = tile_amax(a);
+      uint64_t a2[8];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        a2[2 * s] = pack2(a[s].x, a[s].y);
+        a2[2 * s + 1] = pack2(a[s].z, a[s].w);
+      }
       // 1 / 2^e by its exponent; an infinite maximum leaves no finite scale: every code is NaN
-      const float inv = scale < INFINITY ? __uint_as_float(0x7F000000u - __float_as_uint(scale)) : NAN;
-      uint32_t q[4];
-      if (!WITH_DY && fabsf(w) <= 1e30f) {
-        const float wi = __fmul_rn(w, inv);
+      auto inverse = [](float scale) { return scale < INFINITY ? __uint_as_float(0x7F000000u - __float_as_uint(scale)) : NAN; };
+      auto write_codes = [&](int64_t r, const uint32_t (&q)[4]) {
+        uint8_t* p = dyq + r * d + col;
+        if (WITH_DY) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) *reinterpret_cast<uint32_t*>(p + 32 * s) = q[s];
+        } else {
+          *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      };
+      auto write_folded = [&](int64_t r, float wi) {  // wi = w / scale
         const uint64_t wi2 = pack2(wi, wi);
+        uint32_t q[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const float2 ql = unpack2(mul2(wi2, a2[2 * s])), qh = unpack2(mul2(wi2, a2[2 * s + 1]));
           q[s] = e4m3x4(ql.x, ql.y, qh.x, qh.y);
         }
-      } else {
+        write_codes(r, q);
+      };
+      auto write_row = [&](int64_t r, float w, float inv) {
         const uint64_t w2 = pack2(w, w), inv2 = pack2(inv, inv);
+        uint32_t q[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint64_t lo = mul2(w2, a2[2 * s]), hi = mul2(w2, a2[2 * s + 1]);
@@ -272,55 +297,67 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kCkWarps ? 10 : 2) combin
             *reinterpret_cast<float4*>(dy + r * d + col + kStep * s) = make_float4(vl.x, vl.y, vh.x, vh.y);
           }
         }
+        write_codes(r, q);
+      };
+      if (k0 == 0 && in) {
+        const float scale = pow2_quant_scale(amax), inv = inverse(scale);
+        if (WITH_DY) write_row(P + t, 1.0f, inv);
+        else write_folded(P + t, inv);
+        if ((lane & 7) == 0) dys[(P + t) * tiles + j] = scale;
       }
-      uint8_t* p = dyq + r * d + col;
-      if (WITH_DY) {
+      const float my_scale = pow2_quant_scale(__fmul_rn(fabsf(my_gate), amax));
+      const float my_wi = __fmul_rn(my_gate, inverse(my_scale));
+      if (my_row >= 0 && in) dys[my_tile] = my_scale;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) *reinterpret_cast<uint32_t*>(p + 32 * s) = q[s];
-      } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
-      }
-      if ((lane & 7) == 0) dys[r * tiles + j] = scale;
-    };
-    if (in) write_row(P + t, 1.0f);
-    for (uint32_t left = kept; left;) {
-      const int k = __ffs(left) - 1;
-      left &= left - 1;
-      const uint32_t code[4] = {next.x, next.y, next.z, next.w};
-      const float scale = next_scale;
-      if (left) fetch(left);
-      const int r = __shfl_sync(0xffffffffu, row, k);
-      const float w = __shfl_sync(0xffffffffu, g, k);
-      if (in) write_row(r, w);
-      uint64_t sum2 = pack2(0.f, 0.f);
+      for (int m = 0; m < ROWS; ++m) {
+        const int r = __shfl_sync(0xffffffffu, row, k0 + m);
+        const int from = (lane & 24) | m;
+        const uint32_t code[4] = {next[m % kAhead].x, next[m % kAhead].y, next[m % kAhead].z, next[m % kAhead].w};
+        if (m + kAhead < ROWS) fetch(m + kAhead, next[m % kAhead]);
+        if (r < 0) continue;
+        if (plain) {
+          const float wi = __shfl_sync(0xffffffffu, my_wi, from);
+          if (in) write_folded(r, wi);
+        } else {
+          const float w = __shfl_sync(0xffffffffu, g, k0 + m);
+          if (in) write_row(r, w, inverse(pow2_quant_scale(__fmul_rn(fabsf(w), amax))));
+        }
+        const float scale = __shfl_sync(0xffffffffu, my_ys, from);
+        uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float2 fl = codes_to_float2(code[s] & 0xFFFFu), fh = codes_to_float2(code[s] >> 16);
-        sum2 = fma2(a2[2 * s], pack2(fl.x, fl.y), sum2);
-        sum2 = fma2(a2[2 * s + 1], pack2(fh.x, fh.y), sum2);
-      }
-      const float2 sum = unpack2(sum2);
-      float p = __fmul_rn(__fadd_rn(sum.x, sum.y), scale);
-      // the rest of the sum over the lanes is left to the end
-      p += __shfl_xor_sync(0xffffffffu, p, 16);
-      p += __shfl_xor_sync(0xffffffffu, p, 8);
-      if (lane < 8) {
-        float* at = dot + ((threadIdx.y * warps + warp) * K + k) * 8 + lane;
-        *at = first ? p : *at + p;
+        for (int s = 0; s < 4; ++s) {
+          const float2 fl = codes_to_float2(code[s] & 0xFFFFu), fh = codes_to_float2(code[s] >> 16);
+          sum2 = fma2(a2[2 * s], pack2(fl.x, fl.y), sum2);
+          sum2 = fma2(a2[2 * s + 1], pack2(fh.x, fh.y), sum2);
+        }
+        const float2 sum = unpack2(sum2);
+        mine[32 * m] = fmaf(__fadd_rn(sum.x, sum.y), scale, mine[32 * m]);
       }
     }
-    first = false;
-  }
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) {
+      float p = mine[32 * m];
+      p += __shfl_xor_sync(0xffffffffu, p, 16);
+      p += __shfl_xor_sync(0xffffffffu, p, 8);
+      // the rest of the sum over the lanes is left to the end
+      if (lane < 8 && k0 + m < K) dot[((threadIdx.y * warps + warp) * K + k0 + m) * 8 + lane] = p;
+    }
+    k0 += ROWS;
+  } while (k0 < K);
   __syncthreads();
   if (t < T && threadIdx.x < K) {
     float sum = 0.f;
-    if ((kept >> threadIdx.x) & 1u) {
-      for (int w = 0; w < warps; ++w)
+    for (int w = 0; w < warps; ++w)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += dot[((threadIdx.y * warps + w) * K + threadIdx.x) * 8 + i];
-    }
+      for (int i = 0; i < 8; ++i) sum += dot[((threadIdx.y * warps + w) * K + threadIdx.x) * 8 + i];
     dgate[t * K + threadIdx.x] = sum;
   }
+}
+
+template <int ROWS>
+auto pick_backward(bool with_dy, bool many) {
+  return with_dy ? (many ? combine_checkpoint_backward_kernel<true, kCkMaxWarps, ROWS> : combine_checkpoint_backward_kernel<true, kCkWarps, ROWS>)
+                 : (many ? combine_checkpoint_backward_kernel<false, kCkMaxWarps, ROWS> : combine_checkpoint_backward_kernel<false, kCkWarps, ROWS>);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -374,8 +411,7 @@ extern "C" moe_status moe_combine_checkpoint_backward(const float* dout, const i
     return MOE_ERR_ALIGN;
   const Shape sh = ck_shape(T, K, d / 128);
   const bool many = sh.block.x * sh.block.y > 32 * kCkWarps;
-  auto kern = dy ? (many ? combine_checkpoint_backward_kernel<true, kCkMaxWarps> : combine_checkpoint_backward_kernel<true, kCkWarps>)
-                 : (many ? combine_checkpoint_backward_kernel<false, kCkMaxWarps> : combine_checkpoint_backward_kernel<false, kCkWarps>);
+  auto kern = K > 4 ? pick_backward<8>(dy, many) : (K > 2 ? pick_backward<4>(dy, many) : pick_backward<2>(dy, many));
   kern<<<sh.grid, sh.block, sh.smem, static_cast<cudaStream_t>(stream)>>>(
       dout, dst_of, topk_gate, yq, ys, rows, T, K, d, dyq, dys, dy, dgate, dev_err);
   MOE_CUDA_CHECK_LAUNCH();
