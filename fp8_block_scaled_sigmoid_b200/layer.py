@@ -106,7 +106,8 @@ class MoELayer:
     ``router_grad`` makes forward_train keep what the router's gradient needs
     (the logits, and the expert outputs as an 8-bit checkpoint) and backward
     include the router: du then holds its share too, and the centroids'
-    gradient is returned."""
+    gradient is returned.  backward then refuses to mix two passes: the last
+    one has to be forward_train."""
 
     def __init__(self, cfg: MoEConfig, centroids: torch.Tensor, bias: torch.Tensor,
                  w1q, w1s, w2q, w2s, T: int | None = None, process_group=None,
@@ -148,6 +149,8 @@ class MoELayer:
         self.Y = torch.empty(P + T, d, dtype=f32, device=dev)
         self.out = torch.empty(T, d, dtype=f32, device=dev)
         self.dev_err = torch.zeros(1, dtype=i32, device=dev)
+        # whether idx, gate, logits and the tables are the last forward_train's
+        self._trained = False
         # the grouped GEMMs' work counter (dynamic tile scheduling)
         self.sched = torch.zeros(1, dtype=i32, device=dev)
         self.u_dev = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
@@ -161,6 +164,7 @@ class MoELayer:
     # -- individual steps (also used by the benchmark to time them) --------
     def step_route(self, u):
         c = self.cfg
+        self._trained = False                # what follows belongs to another pass
         _abi.moe_route(u, self.centroids, self.bias, c.G, c.M, c.K, self.idx, self.gate,
                        logits_out=self.logits, ws=self.route_ws, dev_err=self.dev_err,
                        aux=self.balance)
@@ -252,6 +256,7 @@ class MoELayer:
             self.step_combine(u, self.out)
         if update_bias:
             self.step_bias_update()
+        self._trained = True
         return self.out
 
     def step_combine_checkpoint(self, u):
@@ -284,6 +289,8 @@ class MoELayer:
         dcentroids [E][d]; dbalance (fp32, one value per sequence) is the
         upstream gradient of the balance loss of a layer built with
         balance_loss, None where the loss is not trained.
+        A forward in between overwrites the routing: with router_grad that is
+        refused (replays of a captured forward do the same, unseen here).
         Dgrad: dy (1x128 FP8) . W2 -> dh; SwiGLU backward on the cached FP8
         gu -> dgu (1x128 FP8); dgu . W1 -> dx; un-permute.  Wgrad: the
         token-major 128x1 operands dy^T, h^T (recomputed), dgu^T, x^T through
@@ -293,6 +300,9 @@ class MoELayer:
         mark = mark or (lambda name: None)
         if dbalance is not None and not (self.router_grad and self.balance is not None):
             raise _abi.MoEError("backward: dbalance needs a layer built with router_grad and balance_loss")
+        if self.router_grad and not self._trained:
+            raise _abi.MoEError("backward: the last pass of this layer was not forward_train: its routing, and "
+                                "what the router's gradient needs, are gone")
         w1t, w1ts, w2t, w2ts = self.transposed_weights()
         dgate = None
         if self.router_grad:
