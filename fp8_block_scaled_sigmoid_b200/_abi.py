@@ -856,7 +856,9 @@ def moe_combine_checkpoint(Y, dst_of, topk_gate, Y_shared, u, out=None, yq=None,
 def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, dys=None, dy=None,
                                     dgate=None, want_dy=False, dev_err=None, stream=None):
     """dout fp32 [T][d] and the checkpoint (yq, ys) -> (dyq uint8 [T*K+T][d],
-    dys [T*K+T][d/128], dy fp32 or None, dgate fp32 [T][K])."""
+    dys [T*K+T][d/128], dy fp32 or None, dgate fp32 [T][K]).  The rows from
+    T*K on are the shared expert's, so a checkpoint of more rows is refused: of
+    a longer buffer that no pair uses behind T*K, pass the first T*K rows."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq, dys, dy, dgate,
@@ -866,6 +868,9 @@ def moe_combine_checkpoint_backward(dout, dst_of, topk_gate, yq, ys, dyq=None, d
     d = _tiled(what, "dout", dout)[1]
     rows = T * K + T
     n = _width(what, "yq", yq)[0]
+    if n > T * K > 0:
+        raise MoEError(f"{what}: the checkpoint has {n} rows, but there are gradient rows for T*K = {T * K} pairs: "
+                       "pass the first T*K rows if no pair points behind them")
     _dense(what, "dout", dout, _F32, (T, d))
     _dense(what, "topk_gate", topk_gate, _F32, (T, K))
     _dense(what, "yq", yq, _U8, (n, d))

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > kCkWarps ? 2 : (ROWS == 2 
   const int64_t P = static_cast<int64_t>(T) * K;
   int row;
   float g;
-  load_pair(dst_of, gate, t, K, lane, rows < P ? rows : P, t < T, row, g, dev_err);
+  load_pair(dst_of, gate, t, K, lane, rows, t < T, row, g, dev_err);
   if (row < 0) g = 0.f;  // whatever a dropped pair's gate holds
   const int tiles = d / 128, end = t < T ? tiles : 0;
   float* mine = dot + blockDim.y * warps * K * 8 + (threadIdx.y * warps + warp) * 8 * 32 + lane;  // one lane's sums
@@ -403,6 +403,7 @@ extern "C" moe_status moe_combine_checkpoint_backward(const float* dout, const i
   const int64_t P = static_cast<int64_t>(T) * K;
   if (K > kCkMaxK || rows > 0x7FFFFFFFll || P + T > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
+  if (K > 0 && rows > P) return MOE_ERR_SHAPE;  // no gradient row for a pair behind the T*K-th
   if (!dout || !dyq || !dys ||
       (K > 0 && (!dst_of || !topk_gate || !dgate || (rows > 0 && (!yq || !ys)))))
     return MOE_ERR_INVALID_ARG;

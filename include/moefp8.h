@@ -555,11 +555,12 @@ moe_status moe_combine_checkpoint(const float* Y, int64_t rows, const int32_t* d
  * dy) that also gives the gates' gradient from the checkpoint:
  *   dgate[t][k] = sum_j dout[t][j] * yq[r][j] * ys[r][j/128],  r = dst_of[t][k]
  * in fp32 (0 for a negative dst_of).  dyq / dys / dy rows T*K + t are the
- * shared expert's.  An entry >= min(rows, T*K) records MOE_DEVERR_BAD_INDEX
- * and counts as dropped.
+ * shared expert's, so the checkpoint may have T*K rows at most (of a longer
+ * one, pass the first T*K if no pair points behind them).  An entry >= rows
+ * records MOE_DEVERR_BAD_INDEX and counts as dropped.
  *   yq E4M3 [rows][d], ys fp32 [rows][d/128];  dgate fp32 [T][K]
  *   dyq, dys, dy (or NULL) as in moe_combine_backward
- * Limits: d % 128 == 0, 0 <= K <= 32, rows < 2^31, T*K + T < 2^31. */
+ * Limits: d % 128 == 0, 0 <= K <= 32, rows <= T*K (K > 0), T*K + T < 2^31. */
 moe_status moe_combine_checkpoint_backward(const float* dout, const int32_t* dst_of,
                                            const float* topk_gate, const uint8_t* yq,
                                            const float* ys, int64_t rows, int T, int K, int d,

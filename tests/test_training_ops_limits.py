@@ -1,0 +1,31 @@
+"""CPU checks of limits that the training operators' entry points have to keep
+(these calls never reach a GPU)."""
+import pytest
+import torch
+
+from fp8_block_scaled_sigmoid_b200 import _abi
+
+
+def _checkpoint_backward(rows, T=4, K=2):
+    return _abi.lib().moe_combine_checkpoint_backward(16, 16, 16, 16, 16, rows, T, K, 128, 16, 16, None, 16, None, None)
+
+
+@pytest.mark.parametrize("rows", [9, 12, 1 << 30])
+def test_a_checkpoint_of_more_rows_than_pairs_is_refused_by_its_backward(rows):
+    """The gradient rows of T*K pairs are followed by the shared expert's, so a
+    pair at a sorted row behind T*K has no place there: the forward takes such
+    tables, and their backward would lose the pair without a sign."""
+    assert _checkpoint_backward(rows) == 2
+    assert _checkpoint_backward(1 << 31) == 4      # and what was out of range stays so
+
+
+def test_without_pairs_the_checkpoint_may_have_any_rows():
+    assert _checkpoint_backward(9, T=0) == 0
+
+
+def test_the_python_call_says_what_to_do():
+    z = torch.zeros
+    T, K, d = 4, 2, 128
+    with pytest.raises(_abi.MoEError, match=r"pass the first T\*K rows"):
+        _abi.moe_combine_checkpoint_backward(z(T, d), z(T, K, dtype=torch.int32), z(T, K), z(T * K + T, d, dtype=torch.uint8),
+                                             z(T * K + T, 1))
