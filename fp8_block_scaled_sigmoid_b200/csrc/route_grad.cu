@@ -7,7 +7,9 @@
 //     normalisations have the same gradient,
 //       d(sum_k a_k g_k)/dz_i = g_i (1 - s_i) (a_i - sum_j g_j a_j),
 //     with a = dgate for the gates and a = dloss alpha f / S for the balance
-//     loss.  No division by a sum that may be tiny; 1 - s is 1 / (1 + e^z).
+//     loss.  The gates are given, so their sum is not needed; that of all s
+//     is, and where it is tiny the s' come from e^(z - max z).  1 - s is
+//     1 / (1 + e^z).
 //  2. product_kernel -- du = du_base + dz C and dC = dz^T u on the tensor
 //     cores.  u and C are bf16 as they are; dz is fp32, so it is split into
 //     three bf16 terms (hi + mid + lo holds its 24 bits) and every 16 deep step
@@ -168,8 +170,37 @@ __global__ void __launch_bounds__(kRgThreads) dlogits_kernel(
         mean = fmaf(s[j], c[j], mean);
       }
     }
-    const float inv = __fdiv_rn(1.0f, warp_sum(sum));
-    mean = __fmul_rn(warp_sum(mean), inv);
+    sum = warp_sum(sum);
+    mean = warp_sum(mean);
+    if (sum < 0x1p-25f) {
+      // Every s is below 2^-25, where it is e^z to the last bit: the shares are
+      // those of e^(z - max z), which cannot all underflow.
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const int e = 128 * i + 4 * lane;
+        if (e >= E) continue;
+        const float4 v = __ldg(reinterpret_cast<const float4*>(logits + t * E + e));
+        s[4 * i] = v.x;
+        s[4 * i + 1] = v.y;
+        s[4 * i + 2] = v.z;
+        s[4 * i + 3] = v.w;
+        top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      sum = mean = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4 * Q; ++j) {
+        s[j] = 128 * (j / 4) + 4 * lane < E ? expf(__fsub_rn(s[j], top)) : 0.f;
+        sum = __fadd_rn(sum, s[j]);
+        mean = fmaf(s[j], c[j], mean);
+      }
+      sum = warp_sum(sum);
+      mean = warp_sum(mean);
+    }
+    const float inv = __fdiv_rn(1.0f, sum);
+    mean = __fmul_rn(mean, inv);
 #pragma unroll
     for (int j = 0; j < 4 * Q; ++j)
       out[j] = __fmul_rn(__fmul_rn(__fmul_rn(s[j], inv), rest[j]), __fsub_rn(c[j], mean));
