@@ -84,8 +84,11 @@ __global__ void __launch_bounds__(256) half_centroids_kernel(const uint16_t* __r
     const uint4 w = __ldg(row + v);
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+    for (int i = 0; i < 4; ++i) {
+      // an infinite element does not set the scale: the others would vanish
+      const float lo = fabsf(__uint_as_float(x[i] << 16)), hi = fabsf(__uint_as_float(x[i] & 0xFFFF0000u));
+      m = fmaxf(m, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));

@@ -1,5 +1,5 @@
 """GPU checks of the router's gradient at its edges: sigmoids that underflow
-together.
+together, infinite centroids.
 
 "DeepSeek_V3_Report：Annotation", eqs. (13), (15) and (17)-(20).
 """
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp8_block_scaled_sigmoid_b200 as moe
-from tests.test_gpu_route_grad import _case
+from tests.test_gpu_route_grad import _call, _case
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,19 @@ def test_logits_whose_sigmoids_are_all_tiny(cuda_dev, E):
     ref = dz64.T @ c["u"].double()
     bound = (3 * T + 8) * 2.0 ** -23 * (dz64.abs().T @ c["u"].double().abs()) + 2.0 ** -23 * ref.abs()
     assert bool(((dc.double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("T,E", [(200, 144), (4100, 144)])
+def test_an_infinite_centroid_stays_in_its_column(cuda_dev, T, E):
+    """An infinite element of a centroid reaches its own column of du alone:
+    the others have the bits that they have with a zero in its place."""
+    d = 384
+    c = _case(T, E, d, 4, 0, 17, cuda_dev)
+    c["cent"][5, 9] = 0.0
+    want = _call(c, 0)
+    c["cent"][5, 9] = float("inf")
+    got = _call(c, 0)
+    rest = torch.arange(d, device=cuda_dev) != 9
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    assert torch.equal(got[1][:, rest], want[1][:, rest])
+    assert not bool(torch.isfinite(got[1][:, 9]).any())
