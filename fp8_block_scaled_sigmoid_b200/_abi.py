@@ -10,6 +10,7 @@ library is missing or a CUDA device is absent the call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -72,6 +73,7 @@ _SIGS = {
     "moe_combine_checkpoint_backward": (_i, [_p, _p, _p, _p, _p, _i64, _i, _i, _i, _p, _p, _p, _p,
                                              _p, _p]),
     "moe_route_backward_workspace_size": (_i, [_i, _i, _i, _c.POINTER(_sz)]),
+    "moe_route_backward_launches": (_i, [_i, _i, _i, _i, _i, _c.POINTER(_i)]),
     "moe_route_backward": (_i, [_p, _p, _p, _p, _p, _i64, _p, _i, _i, _i, _i, _p, _p, _i, _f, _p,
                                 _p, _p, _p, _p, _sz, _p, _p]),
 }
@@ -109,7 +111,8 @@ DEVERR = {0: "none", 1: "bounded wait timed out", 2: "inconsistent segment table
 
 _lib = None
 
-# Kernels each entry point launches (for the benchmark's launch count).
+# Kernels each entry point launches (for the benchmark's launch count;
+# moe_route_backward's depend on its sizes).
 LAUNCHES_PER_CALL = {"fp8_quant_1x128": 1, "fp8_quant_128x128": 1, "swiglu_quant": 1,
                      "swiglu_quant_pow2": 1,
                      "fp8_quant_1x128_pow2": 1, "fp8_quant_128x128_pow2": 1,
@@ -124,7 +127,7 @@ LAUNCHES_PER_CALL = {"fp8_quant_1x128": 1, "fp8_quant_128x128": 1, "swiglu_quant
                      "moe_seq_balance_loss": 3, "moe_fp8_mma_peak": 1,
                      "moe_sort_rows": 1, "moe_sort_rows_backward": 1, "moe_unsort_rows": 1,
                      "moe_unsort_rows_backward": 1, "moe_combine_checkpoint": 1,
-                     "moe_combine_checkpoint_backward": 1, "moe_route_backward": 3}
+                     "moe_combine_checkpoint_backward": 1}
 launch_count = 0
 
 
@@ -907,6 +910,14 @@ def moe_route_backward_workspace_size(T, d, E) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _route_backward_launches(device, T, d, E, dcentroids) -> int:
+    """Kernels of a call with du (they depend on the device's SM count)."""
+    n = _i(0)
+    _check(lib().moe_route_backward_launches(T, d, E, 1, dcentroids, ctypes.byref(n)), "moe_route_backward_launches")
+    return n.value
+
+
 def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base=None, f=None,
                        dloss=None, alpha=1e-4, seq_len=0, dlogits=None, du=None, dcentroids=None,
                        ws=None, want_dcentroids=True, dev_err=None, stream=None):
@@ -955,10 +966,11 @@ def moe_route_backward(dgate, logits, topk_idx, topk_gate, u, centroids, du_base
         dcentroids = logits.new_empty((E, d))
     if ws is None:
         ws = logits.new_empty(moe_route_backward_workspace_size(T, d, E), dtype=_U8)
-    _count(what)
     _check(lib().moe_route_backward(
         _addr(dgate), logits.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), u.data_ptr(), ldu,
         centroids.data_ptr(), T, d, E, K, _addr(f), _addr(dloss), seq_len, alpha, _addr(du_base),
         dlogits.data_ptr(), du.data_ptr(), _addr(dcentroids), ws.data_ptr(), ws.nbytes,
         _addr(dev_err), st), what)
+    global launch_count
+    launch_count += _route_backward_launches(logits.get_device(), T, d, E, int(dcentroids is not None))
     return dlogits, du, dcentroids

@@ -860,6 +860,16 @@ extern "C" moe_status moe_route_backward_workspace_size(int T, int d, int E, siz
   return MOE_OK;
 }
 
+extern "C" moe_status moe_route_backward_launches(int T, int d, int E, int du, int dcentroids, int* launches) {
+  if (!launches) return MOE_ERR_INVALID_ARG;
+  const moe_status s = moe::check_sizes(T, d, E);
+  if (s != MOE_OK) return s;
+  const moe::Plan plan = moe::make_plan(T, d, E, du != 0, dcentroids != 0);
+  if (!plan.fits) return MOE_ERR_UNSUPPORTED;
+  *launches = T == 0 ? 0 : plan.half_du + 1 + (dcentroids != 0) + (du != 0) + (plan.parts != 0);
+  return MOE_OK;
+}
+
 extern "C" moe_status moe_route_backward(
     const float* dgate, const float* logits, const int32_t* topk_idx, const float* topk_gate,
     const uint16_t* u, int64_t ldu, const uint16_t* centroids, int T, int d, int E, int K,

@@ -593,6 +593,8 @@ moe_status moe_combine_checkpoint_backward(const float* dout, const int32_t* dst
  * K <= 32), ldu % 8 == 0, T % seq_len == 0.
  */
 moe_status moe_route_backward_workspace_size(int T, int d, int E, size_t* bytes);
+/* Kernels that a call launches, which its sizes and the gradients wanted decide. */
+moe_status moe_route_backward_launches(int T, int d, int E, int du, int dcentroids, int* launches);
 moe_status moe_route_backward(const float* dgate, const float* logits, const int32_t* topk_idx,
                               const float* topk_gate, const uint16_t* u, int64_t ldu,
                               const uint16_t* centroids, int T, int d, int E, int K,

@@ -1,5 +1,7 @@
 """CPU checks of limits that the training operators' entry points have to keep
 (these calls never reach a GPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -29,3 +31,13 @@ def test_the_python_call_says_what_to_do():
     with pytest.raises(_abi.MoEError, match=r"pass the first T\*K rows"):
         _abi.moe_combine_checkpoint_backward(z(T, d), z(T, K, dtype=torch.int32), z(T, K), z(T * K + T, d, dtype=torch.uint8),
                                              z(T * K + T, 1))
+
+
+def test_launches_of_the_router_gradient():
+    L, n = _abi.lib(), ctypes.c_int(-1)
+    call = lambda T, d, E, du=1, dc=1: L.moe_route_backward_launches(T, d, E, du, dc, ctypes.byref(n))
+    assert call(0, 256, 32) == 0 and n.value == 0
+    assert call(40, 256, 32, 0, 0) == 0 and n.value == 1       # dlogits alone
+    assert call(4608, 384, 272, 1, 0) == 0 and n.value == 3    # half operands: the centroids' conversion too
+    assert call(40, 256, 2048) == 4 and call(40, 250, 32) == 2 and call(-1, 256, 32) == 1
+    assert L.moe_route_backward_launches(40, 256, 32, 1, 1, None) == 1
