@@ -10,14 +10,15 @@
 //     loss.  The gates are given, so their sum is not needed; that of all s
 //     is, and where it is tiny the s' come from e^(z - max z).  1 - s is
 //     1 / (1 + e^z).
-//  2. product_kernel -- du = du_base + dz C and dC = dz^T u on the tensor
+//  2. products_kernel -- du = du_base + dz C and dC = dz^T u on the tensor
 //     cores.  u and C are bf16 as they are; dz is fp32, so it is split into
 //     three bf16 terms (hi + mid + lo holds its 24 bits) and every 16 deep step
 //     of the product takes three MMAs.  Two terms would lose 2^-17 of a
 //     gradient, which the router keeps in high precision.  For many tokens du
 //     takes scaled half operands and two terms instead (half_centroids_kernel).
-//     The two products run side by side, each on its share of the SMs
-//     (make_plan): du waits for memory while dC waits for the tensor cores.
+//     The two products run side by side in one launch, each on its share of
+//     the SMs (make_plan): du waits for memory while dC waits for the tensor
+//     cores.
 //  3. reduce_kernel -- where the depth T of dC's tiles is split over CTAs, their
 //     parts are added in a fixed order.
 #include <cuda_bf16.h>
@@ -351,7 +352,6 @@ struct ProductArgs {
   int per;       // depth blocks of a CTA; 0: whole tiles, evenly
   int first, share;  // whole tiles: the first CTAs take this many, the others the rest
   int has_base;
-  int after_dc;  // du launched behind dC
   const float* row_scale;  // of half terms
   int32_t* dev_err;
 };
@@ -435,11 +435,16 @@ __global__ void __launch_bounds__(64) reduce_kernel(const Parts a) {
   }
 }
 
+// One product and where it reads and writes.
+struct Product {
+  CUtensorMap a, b, base, out, part;
+  ProductArgs args;
+};
+
+// CTA `cta` of the product's `ctas`.
 template <bool A_MN, int TERMS>
-__global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
-    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-    const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmOut,
-    const __grid_constant__ CUtensorMap tmPart, const ProductArgs args) {
+__device__ __forceinline__ void run_product(const Product& pr, const int cta, const int ctas) {
+  const ProductArgs& args = pr.args;
   using R = Ring<A_MN, TERMS>;
   constexpr int kStages = R::kStages, kPatches = R::kPatches;
   extern __shared__ uint8_t smem_raw[];
@@ -469,9 +474,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
-    prefetch_tmap(&tmOut);
+    prefetch_tmap(&pr.a);
+    prefetch_tmap(&pr.b);
+    prefetch_tmap(&pr.out);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kPrTmemCols);
@@ -482,19 +487,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile int* abort_v = abort_flag;
-  // dC, and du without dC before it, need the terms that their predecessor
-  // writes.  du after dC finds them complete, since dC lets it start only once
-  // it has them itself; it runs beside dC and must only not end before it.
-  if (!args.after_dc) wait_predecessor();
+  wait_predecessor();  // dz's terms
   if (A_MN) launch_dependents();
   int start, end;
   if (args.per) {
-    start = min(args.units, static_cast<int>(blockIdx.x) * args.per);
+    start = min(args.units, cta * args.per);
     end = min(args.units, start + args.per);
   } else {
     const int64_t tiles = args.units / args.KB;
-    const bool early = static_cast<int>(blockIdx.x) < args.first;
-    const int64_t b = early ? blockIdx.x : blockIdx.x - args.first, n = early ? args.first : gridDim.x - args.first;
+    const bool early = cta < args.first;
+    const int64_t b = early ? cta : cta - args.first, n = early ? args.first : ctas - args.first;
     const int64_t t0 = early ? 0 : args.share, nt = early ? args.share : tiles - args.share;
     start = static_cast<int>(t0 + nt * b / n) * args.KB;
     end = static_cast<int>(t0 + nt * (b + 1) / n) * args.KB;
@@ -519,14 +521,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
           uint8_t* sB = sA + TERMS * kPrTerm;
           mbar_arrive_expect_tx(&full[s], R::kStage);
           if (A_MN) {  // [64 experts][term][depth][64]
-            tma_load_3d(sA, &tmA, &full[s], g.m0, kb * kPrK, 0);
-            tma_load_3d(sA + TERMS * kPrSlab, &tmA, &full[s], g.m0 + 64, kb * kPrK, 0);
+            tma_load_3d(sA, &pr.a, &full[s], g.m0, kb * kPrK, 0);
+            tma_load_3d(sA + TERMS * kPrSlab, &pr.a, &full[s], g.m0 + 64, kb * kPrK, 0);
           } else {     // [term][row][depth]
-            tma_load_3d(sA, &tmA, &full[s], kb * kPrK, g.m0, 0);
+            tma_load_3d(sA, &pr.a, &full[s], kb * kPrK, g.m0, 0);
           }
 #pragma unroll
           for (int j = 0; j < kPrN / 64; ++j)
-            tma_load_2d(sB + j * kPrSlab, &tmB, &full[s], g.n0 + 64 * j, kb * kPrK);
+            tma_load_2d(sB + j * kPrSlab, &pr.b, &full[s], g.n0 + 64 * j, kb * kPrK);
         }
       }
       // every issued copy lands before the CTA can exit
@@ -576,8 +578,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       }
       mma_commit(done);
       mbar_wait(done, 0, nullptr, args.dev_err);
-    } else if (!A_MN && warp == 2) {
-      if (args.after_dc) wait_predecessor();
     }
     __syncwarp();
   } else {
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       if (lt >= t1) return;
       const int b = loads % kPatches;
       mbar_arrive_expect_tx(&landed[b], kPrPatch);
-      tma_load_2d(patch + b * kPrPatch, &tmBase, &landed[b], lt / args.mt * kPrN + half * 128 + 32 * lb,
+      tma_load_2d(patch + b * kPrPatch, &pr.base, &landed[b], lt / args.mt * kPrN + half * 128 + 32 * lb,
                   lt % args.mt * kPrM + quarter * 32);
       ++loads;
       if (++lb == 4) {
@@ -642,8 +642,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
       // whole tiles go to the result, the part of one to the CTA's place
       const bool direct = !A_MN || g.whole;
       if (direct && (g.n0 + half * 128 >= args.N || g.m0 + quarter * 32 >= args.M)) continue;
-      const CUtensorMap* dst = direct ? &tmOut : &tmPart;
-      const int row0 = direct ? g.m0 + quarter * 32 : static_cast<int>(blockIdx.x) * kPrM + quarter * 32;
+      const CUtensorMap* dst = direct ? &pr.out : &pr.part;
+      const int row0 = direct ? g.m0 + quarter * 32 : cta * kPrM + quarter * 32;
       const int col0 = direct ? g.n0 + half * 128 : half * 128;
 #pragma unroll
       for (int b = 0; b < 4; ++b, ++used) {
@@ -691,6 +691,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) product_kernel(
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, kPrTmemCols);
 }
+
+// Both products in one launch: dC's CTAs come first, du's take the other SMs and
+// those that dC leaves.  (As two launches du would read terms that only dC has
+// waited for.)
+template <int DU_TERMS>
+__global__ void __launch_bounds__(kPrThreads, 1) products_kernel(const __grid_constant__ Product dc,
+                                                                 const __grid_constant__ Product du,
+                                                                 const int dc_ctas) {
+  const int cta = blockIdx.x;
+  if (cta < dc_ctas) run_product<true, 3>(dc, cta, dc_ctas);
+  else run_product<false, DU_TERMS>(du, cta - dc_ctas, static_cast<int>(gridDim.x) - dc_ctas);
+}
+template <int DU_TERMS>
+constexpr int kPrSmem = std::max(Ring<true, 3>::kSmem, Ring<false, DU_TERMS>::kSmem);
 
 // Launches a kernel, behind: before the one ahead of it has ended.
 template <typename... P, typename... A>
@@ -828,9 +842,8 @@ bool grant_smem() {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (dev >= 0 && dev < 64 && done[dev]) return true;
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if (cudaFuncSetAttribute(product_kernel<true, 3>, attr, Ring<true, 3>::kSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(product_kernel<false, 3>, attr, Ring<false, 3>::kSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(product_kernel<false, 2>, attr, Ring<false, 2>::kSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(products_kernel<3>, attr, kPrSmem<3>) != cudaSuccess ||
+      cudaFuncSetAttribute(products_kernel<2>, attr, kPrSmem<2>) != cudaSuccess)
     return false;
   if (dev >= 0 && dev < 64) done[dev] = true;
   return true;
@@ -866,7 +879,7 @@ extern "C" moe_status moe_route_backward_launches(int T, int d, int E, int du, i
   if (s != MOE_OK) return s;
   const moe::Plan plan = moe::make_plan(T, d, E, du != 0, dcentroids != 0);
   if (!plan.fits) return MOE_ERR_UNSUPPORTED;
-  *launches = T == 0 ? 0 : plan.half_du + 1 + (dcentroids != 0) + (du != 0) + (plan.parts != 0);
+  *launches = T == 0 ? 0 : plan.half_du + 1 + (du || dcentroids) + (plan.parts != 0);
   return MOE_OK;
 }
 
@@ -928,34 +941,33 @@ extern "C" moe_status moe_route_backward(
   const auto fp16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const uint64_t rd = static_cast<uint64_t>(d) * 4, rz = static_cast<uint64_t>(E) * 2;
   const uint64_t stride[2] = {rz, rz * T};
-  CUtensorMap a, b, in, out, part;
+  Product pc{}, pu{};
+  const int dc_ctas = dcentroids ? plan.dc_ctas : 0, du_ctas = du ? plan.du_ctas : 0;
   if (dcentroids) {
     const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), 3};
     const uint32_t box[3] = {64, kPrK, 3};
-    if (!moe_make_tmap_3d(&a, bf16_terms, bf16, extent, stride, box, 128) ||
-        !moe_make_tmap_2d(&b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
-        !moe_make_tmap_2d(&out, dcentroids, fp32, d, E, rd, 32, 32) ||
-        (plan.parts && !moe_make_tmap_2d(&part, parts, fp32, kPrN, static_cast<uint64_t>(plan.dc_ctas) * kPrM, kPrN * 4, 32, 32)))
+    if (!moe_make_tmap_3d(&pc.a, bf16_terms, bf16, extent, stride, box, 128) ||
+        !moe_make_tmap_2d(&pc.b, u, bf16, d, T, static_cast<uint64_t>(ldu) * 2, 64, kPrK) ||
+        !moe_make_tmap_2d(&pc.out, dcentroids, fp32, d, E, rd, 32, 32) ||
+        (plan.parts && !moe_make_tmap_2d(&pc.part, parts, fp32, kPrN, static_cast<uint64_t>(plan.dc_ctas) * kPrM, kPrN * 4, 32, 32)))
       return MOE_ERR_CUDA;
-    if (!plan.parts) part = out;  // not used
-    const ProductArgs args{E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, 0, 0, nullptr, dev_err};
-    if (!launch(product_kernel<true, 3>, plan.dc_ctas, kPrThreads, Ring<true, 3>::kSmem, true, st, a, b, out, out, part, args))
-      return MOE_ERR_CUDA;
+    pc.args = {E, d, plan.dc_kb, plan.dc_mt, plan.dc_units, plan.dc_per, 0, 0, 0, nullptr, dev_err};
   }
   if (du) {
     const uint32_t n = half_du ? 2 : 3;
     const uint64_t extent[3] = {static_cast<uint64_t>(E), static_cast<uint64_t>(T), n};
     const uint32_t box[3] = {kPrK, kPrM, n};
-    if (!moe_make_tmap_3d(&a, half_du ? half_terms : bf16_terms, half_du ? fp16 : bf16, extent, stride, box, 64) ||
-        !moe_make_tmap_2d(&b, half_du ? half_cent : centroids, half_du ? fp16 : bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK) ||
-        !moe_make_tmap_2d(&in, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
-        !moe_make_tmap_2d(&out, du, fp32, d, T, rd, 32, 32))
+    if (!moe_make_tmap_3d(&pu.a, half_du ? half_terms : bf16_terms, half_du ? fp16 : bf16, extent, stride, box, 64) ||
+        !moe_make_tmap_2d(&pu.b, half_du ? half_cent : centroids, half_du ? fp16 : bf16, d, E, static_cast<uint64_t>(d) * 2, 64, kPrK) ||
+        !moe_make_tmap_2d(&pu.base, du_base ? du_base : du, fp32, d, T, rd, 32, 32) ||
+        !moe_make_tmap_2d(&pu.out, du, fp32, d, T, rd, 32, 32))
       return MOE_ERR_CUDA;
-    const ProductArgs args{T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, plan.du_first, plan.du_share,
-                           du_base ? 1 : 0, dcentroids ? 1 : 0, row_scale, dev_err};
+    pu.args = {T, d, plan.du_kb, plan.du_mt, plan.du_units, 0, plan.du_first, plan.du_share, du_base ? 1 : 0, row_scale, dev_err};
+  }
+  if (dc_ctas + du_ctas > 0) {
     const bool ok = half_du
-        ? launch(product_kernel<false, 2>, plan.du_ctas, kPrThreads, Ring<false, 2>::kSmem, true, st, a, b, in, out, out, args)
-        : launch(product_kernel<false, 3>, plan.du_ctas, kPrThreads, Ring<false, 3>::kSmem, true, st, a, b, in, out, out, args);
+        ? launch(products_kernel<2>, dc_ctas + du_ctas, kPrThreads, kPrSmem<2>, true, st, pc, pu, dc_ctas)
+        : launch(products_kernel<3>, dc_ctas + du_ctas, kPrThreads, kPrSmem<3>, true, st, pc, pu, dc_ctas);
     if (!ok) return MOE_ERR_CUDA;
   }
   if (plan.parts) {
