@@ -724,12 +724,20 @@ bool launch(void (*kern)(P...), int64_t grid, int block, int smem, bool behind, 
   return false;
 }
 
-// Tokens and experts above which du takes half operands: the call takes 412 us
-// against 437 so at 16384 tokens x 384 experts x 7168, 154 against 165 at 6000,
-// but 114 against 116 at 4096 and 96 against 88 there with 256 experts, where
-// converting the centroids first costs what the product saves.  With few experts
-// du waits for memory either way (16384 x 128 x 4096: 151 against 149).
-constexpr int kHalfAbove = 4096, kHalfExperts = 128;
+// When du takes half operands: above 4096 tokens, with more than 256 experts or
+// where tokens x experts, the work saved, outweigh converting the centroids.  A
+// call from one graph, three bf16 terms / two half terms, us, rows of 7168:
+//   experts     128        160        256        304        384        512        1024
+//   4100     79 /  83  100 / 103   91 /  99  112 / 107  124 / 121  175 / 164  322 / 293
+//   8192    131 / 135  175 / 175  182 / 184  208 / 230  222 / 205  305 / 284  589 / 514
+//   16384   260 / 260  330 / 327  332 / 315  440 / 416  452 / 426  608 / 537 1183 / 1016
+// (4608 for 4100 with 128, 160, 512 and 1024 experts.)  Up to 128 experts du waits
+// for memory either way.  At 4096 tokens and fewer the halves gain little (384
+// experts: 117 / 114 at 4096, 68 / 64 at 2048, 41 / 44 at 1024), and three terms
+// hold two bits more.
+bool half_operands(int T, int E) {
+  return T > 4096 && (E > 256 || (E > 128 && static_cast<int64_t>(T) * E > 1 << 21));
+}
 
 struct Plan {
   // workspace bytes: dz in bf16 and in half terms, the centroids in half, the
@@ -817,7 +825,7 @@ Plan make_plan(int T, int d, int E, bool du, bool dc) {
   const int64_t tm = (static_cast<int64_t>(T) + kPrM - 1) / kPrM, tk = (static_cast<int64_t>(T) + kPrK - 1) / kPrK;
   const int64_t em = (E + kPrM - 1) / kPrM, ek = (E + kPrK - 1) / kPrK;
   const int64_t units = tm * nt * ek;
-  p.half_du = du && T > kHalfAbove && E > kHalfExperts;
+  p.half_du = du && half_operands(T, E);
   p.du_units = static_cast<int>(units);
   p.du_kb = static_cast<int>(ek);
   p.du_mt = static_cast<int>(tm);

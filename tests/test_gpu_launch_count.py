@@ -20,8 +20,8 @@ def _nodes(graph):
 
 
 @pytest.mark.parametrize("T,E,d,want_dc", [
-    (40, 32, 256, True), (200, 256, 7168, True), (200, 256, 7168, False), (4608, 272, 384, True),
-    (4608, 272, 384, False), (6000, 128, 2048, True),
+    (40, 32, 256, True), (200, 256, 7168, True), (200, 256, 7168, False), (4608, 384, 384, True),
+    (4608, 384, 384, False), (6000, 128, 2048, True),
 ])
 def test_route_backward_counts_its_kernels(cuda_dev, T, E, d, want_dc):
     c = _case(T, E, d, 4, 0, 3, cuda_dev)

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("T,E,G,M,K,pow2,S", [(264, 16, 4, 2, 4, True, 88), (1024, 32, 4, 2, 8, False, 256),
-                                              (4224, 144, 1, 1, 4, True, 528)])
+                                              (4224, 368, 1, 1, 4, True, 528)])
 def test_training_step_with_the_router(cuda_dev, T, E, G, M, K, pow2, S):
     cfg = configs.TINY.with_(name="router_step", T=T, d=256, E=E, G=G, M=M, K=K, I=256)
     w = make_fp8_weights(cfg, cuda_dev, pow2=pow2)

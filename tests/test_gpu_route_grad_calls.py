@@ -8,8 +8,8 @@ from tests.test_gpu_route_grad import _call, _case, _check
 
 pytestmark = pytest.mark.gpu
 
-# both products side by side: dC in parts, dC whole, du from half operands with dC in parts and whole
-SIZES = [(1024, 256, 7168, 8), (3000, 16, 128, 2), (4608, 272, 384, 8), (5000, 144, 4352, 4)]
+# both products side by side: dC whole, dC in parts, du from half operands with dC in parts and whole
+SIZES = [(1024, 256, 7168, 8), (3000, 16, 128, 2), (4608, 384, 384, 8), (4200, 384, 7168, 4)]
 
 
 def _raw(c, dlogits, du, dc):

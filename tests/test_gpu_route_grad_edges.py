@@ -6,6 +6,7 @@ together, infinite centroids.
 import pytest
 import torch
 
+import tests.test_gpu_route_grad as base
 import fp8_block_scaled_sigmoid_b200 as moe
 from tests.test_gpu_route_grad import _call, _case
 
@@ -49,7 +50,7 @@ def test_logits_whose_sigmoids_are_all_tiny(cuda_dev, E):
     assert bool(((dc.double() - ref).abs() <= bound).all())
 
 
-@pytest.mark.parametrize("T,E", [(200, 144), (4100, 144)])
+@pytest.mark.parametrize("T,E", [(200, 144), (4100, 144), (4100, 384)])
 def test_an_infinite_centroid_stays_in_its_column(cuda_dev, T, E):
     """An infinite element of a centroid reaches its own column of du alone:
     the others have the bits that they have with a zero in its place."""
@@ -63,3 +64,9 @@ def test_an_infinite_centroid_stays_in_its_column(cuda_dev, T, E):
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     assert torch.equal(got[1][:, rest], want[1][:, rest])
     assert not bool(torch.isfinite(got[1][:, 9]).any())
+
+
+@pytest.mark.parametrize("E", [384, 400])
+def test_uneven_scales_with_more_experts(cuda_dev, E):
+    """Where du is the product of half operands."""
+    base.test_many_tokens_with_uneven_scales(cuda_dev, E)

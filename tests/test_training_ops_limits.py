@@ -38,6 +38,15 @@ def test_launches_of_the_router_gradient():
     call = lambda T, d, E, du=1, dc=1: L.moe_route_backward_launches(T, d, E, du, dc, ctypes.byref(n))
     assert call(0, 256, 32) == 0 and n.value == 0
     assert call(40, 256, 32, 0, 0) == 0 and n.value == 1       # dlogits alone
-    assert call(4608, 384, 272, 1, 0) == 0 and n.value == 3    # half operands: the centroids' conversion too
+    assert call(4608, 384, 400, 1, 0) == 0 and n.value == 3    # half operands: the centroids' conversion too
     assert call(40, 256, 2048) == 4 and call(40, 250, 32) == 2 and call(-1, 256, 32) == 1
     assert L.moe_route_backward_launches(40, 256, 32, 1, 1, None) == 1
+
+
+@pytest.mark.parametrize("T,E,half", [(4096, 1024, 0), (4097, 272, 1), (4100, 256, 0), (8192, 256, 0), (8200, 256, 1),
+                                      (16384, 128, 0), (14000, 144, 0), (16384, 144, 1)])
+def test_where_the_input_gradient_takes_half_operands(T, E, half):
+    """Three terms where halves do not pay: their conversion is a kernel more."""
+    n = ctypes.c_int(-1)
+    assert _abi.lib().moe_route_backward_launches(T, 384, E, 1, 0, ctypes.byref(n)) == 0
+    assert n.value == 2 + half
