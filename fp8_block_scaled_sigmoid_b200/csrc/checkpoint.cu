@@ -13,9 +13,10 @@
 // 16-byte one and a tile's maximum takes three shuffles for 16 values a lane
 // (one lane per 4 values would take five).  The forward's pieces are CTAs' warps
 // in any order; the backward's share a CTA a token, for the sums of dgate.
-// One B200, 4096 tokens x 8 experts x 7168: the combine with its checkpoint 238
-// us, 96% of the measured copy rate (HBM bound); its backward 109 us, 90%, and 285
-// us, 92%, with the fp32 rows as well.
+// One B200, 4096 tokens x 8 experts x 7168, one of several launches in a graph: the
+// combine with its checkpoint 238 us, 96% of the measured copy rate (HBM bound); its
+// backward 109 us, 90%, and 284 us, 92%, with the fp32 rows as well (in a loop 2 to
+// 6 us more).
 #include <cuda_fp8.h>
 
 #include "epi_math.cuh"

@@ -14,8 +14,9 @@
 //     cores.  u and C are bf16 as they are; dz is fp32, so it is split into
 //     three bf16 terms (hi + mid + lo holds its 24 bits) and every 16 deep step
 //     of the product takes three MMAs.  Two terms would lose 2^-17 of a
-//     gradient, which the router keeps in high precision.  For many tokens du
-//     takes scaled half operands and two terms instead (half_centroids_kernel).
+//     gradient, which the router keeps in high precision.  For many tokens and
+//     experts (half_operands) du takes scaled half operands and two terms
+//     instead (half_centroids_kernel).
 //     The two products run side by side in one launch, each on its share of
 //     the SMs (make_plan): du waits for memory while dC waits for the tensor
 //     cores.
@@ -754,10 +755,12 @@ struct Plan {
 // (one CTA each, the depth padded with blocks of zeros).  du's CTAs have the
 // other SMs from the start, with so many tiles each that they end with those that
 // get in when dC's CTAs leave.  Of all these the one that ends first by the
-// following times (in 10 ns, measured) is taken.
-// 4096 tokens x 256 experts x 7168 take 88 us so and 99 with each product on the
-// whole GPU in turn, 16384 x 384 412 and 437, 1024 x 256 31 and 39, 6000 x 64 x
-// 2048 36 and 72.
+// following times (in 10 ns, measured at full clock) is taken.
+// From one graph 4096 tokens x 256 experts x 7168 take 87 us so and 99 with each
+// product on the whole GPU in turn, 16384 x 384 405 and 437, 1024 x 256 29 and 39,
+// 6000 x 64 x 2048 35 and 72.  Under the power cap the clock falls and dC, bound by
+// the tensor cores, slows more than du, bound by memory: 16384 x 384 in a long loop
+// takes 430 to 450.
 constexpr int kDcBlock = 64, kDcPart = 250;     // a depth block; a tile's or a part's result
 constexpr int kDuTile = 150, kDuBlock3 = 85, kDuBlock2 = 57, kDuLeast = 600;  // a tile; HBM's share of it
 constexpr int kAdd = 500, kAddPart = 16;        // reduce_kernel; each part of a tile
@@ -780,7 +783,7 @@ void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_
       // late tiles by each CTA that comes after dC's, early ones by the others
       const int64_t ideal = (du_tiles * du_cost + ctas * dc_end) / sms;
       const int64_t guess = std::max<int64_t>(0, (ideal - dc_end) / du_cost);
-      end = INT64_MAX;
+      end = INT64_MAX;  // with no free SM, guess + 1 late tiles a CTA are all there are
       for (int64_t late = guess; late <= guess + 1; ++late) {
         const int64_t rest = std::max<int64_t>(0, du_tiles - late * ctas);
         if (free == 0 && rest > 0) continue;
@@ -791,11 +794,6 @@ void plan_products(Plan& p, bool du, bool dc, int64_t sms, int64_t tiles, int64_
         first = rest == du_tiles ? 0 : std::min(free, rest);
         share = first ? rest : 0;
         on = first ? first + std::min(ctas, du_tiles - rest) : std::min(late ? ctas : free, du_tiles);
-      }
-      if (end == INT64_MAX) {  // no free SM, and more than a tile late
-        const int64_t late = (du_tiles + ctas - 1) / ctas;
-        end = dc_end + late * du_cost;
-        on = std::min(sms, du_tiles);
       }
     }
     if (end + add >= best) return;

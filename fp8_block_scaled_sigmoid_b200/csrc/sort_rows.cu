@@ -10,12 +10,15 @@
 // Two shapes of kernel: a scatter (one token row to K sorted rows) and a
 // gather (K sorted rows to one token row).  Both are bound by HBM: every row
 // is read once and written once, with a few fp32 operations an element.  A
-// warp takes one stretch of a token's columns through all of its K rows, eight
-// accesses a lane at a time: the loads of several sorted rows are in flight
-// together, and the token's values stay in registers as the words they were read
-// as (as separate 16-bit elements they cost twice the registers, and with them
-// half the warps that hide the latency).
-// One B200, rows of 7168 in bf16, of the measured copy rate of 6.44 TB/s:
+// warp takes one stretch of a token's columns through all of its K rows: where
+// sorted rows are read, the loads of several are in flight together (accesses a
+// lane: the gather 8, or 16 of 4 bytes; the dot products 4, or 8 narrow ones; the
+// scatter reads one token row, 1 to 8 accesses, for its K rows of stores), and the
+// token's values stay in registers as the words they were read as (as separate
+// 16-bit elements they cost twice the registers, and with them half the warps that
+// hide the latency).
+// One B200, rows of 7168 in bf16, one of several launches in a graph, of the
+// measured copy rate of 6.44 TB/s (a call in a loop takes about 2 us more):
 //   sort            4096 tokens x 8: 87 us, 95%     its backward:    83 us, 99%
 //   unsort backward 16384 x 6:      474 us, 100%    one token's sort: 1.8 us
 #include <cuda_bf16.h>
@@ -29,7 +32,7 @@ namespace {
 constexpr int kSrMaxK = 32;
 constexpr int kSrWarps = 4;      // warps of a CTA, each with a piece of its own
 constexpr int kSrDotWarps = 16;  // most warps of a CTA whose warps share a token
-constexpr int kSrFlight = 8;     // accesses a lane has in flight: U columns x kSrFlight / U rows
+constexpr int kSrFlight = 8;     // 16-byte accesses a lane of the gather has in flight: U columns x kSrFlight / U rows
 
 // Columns and rows a lane of the dot kernel has in flight: fewer than elsewhere,
 // so that 32 warps an SM fit (16384 x 6: 474 us; four columns 597).
@@ -366,10 +369,11 @@ void with_unroll(int K, F&& fn) {
 }
 
 // fn(Access<T, N, U>) for the call's element type and the bytes (16, 4 or one
-// element) that every row involved is aligned to and made of.  U columns of
-// few rows or one column of many: either way eight loads a lane are in flight.
-// Narrow accesses take two rows of U columns: sort backward of 4096 x 8 rows in
-// bf16 takes 83 us at a width of 7168, 81 at 7002 and 146 at 7001.
+// element) that every row involved is aligned to and made of.  The gather has U
+// columns of few rows or one column of many in flight, of narrow accesses U columns
+// of two rows.  With fewer bytes in each access there are fewer in flight and more
+// instructions: 4096 x 8 rows in bf16 at widths of 7168, 7002 and 7001 take the sort's
+// backward 83, 83 and 146 us, the unsort's 164, 266 and 362.
 template <typename F>
 void with_access(moe_dtype dt, int bytes, int K, F&& fn) {
   if (dt == MOE_BF16) {

@@ -535,7 +535,8 @@ moe_status moe_unsort_rows_backward(const void* dout, moe_dtype dtype, int64_t l
  * The combine with an 8-bit checkpoint of the expert outputs.  The gates'
  * gradient, dgate[t][k] = dout[t] . Y[dst_of[t][k]], needs Y in the backward;
  * the checkpoint keeps it in E4M3 with 1x128 scales (a quarter of the fp32
- * rows) as [ANN] "Low-Precision Activation" keeps the SwiGLU input.
+ * rows) as [ANN] "Low-Precision Activation" keeps the SwiGLU input.  dst_of is
+ * a table of distinct rows; no buffer written may overlap one read.
  * =========================================================================== */
 
 /* moe_combine_checkpoint -- moe_combine that also leaves the checkpoint:
@@ -586,9 +587,16 @@ moe_status moe_combine_checkpoint_backward(const float* dout, const int32_t* dst
  *   dlogits fp32 [T][E], du fp32 [T][d], dcentroids fp32 [E][d], each or NULL
  *   (not computed);  ws: moe_route_backward_workspace_size() bytes, one call
  *   at a time
- * fp32 arithmetic throughout; the result does not depend on timing.  An index
- * outside [0, E) records MOE_DEVERR_BAD_INDEX and its gate part is left out.
- * T == 0 sets dcentroids to zero.
+ * dlogits, and the sums of du and dcentroids, are fp32; the result does not
+ * depend on timing.  In the products the tensor cores take dlogits as three
+ * bf16 terms (24 bits; u and centroids as they are), and for du of many tokens
+ * and experts (T > 4096 and E > 256, or E > 128 and T*E > 2^21) as two half
+ * terms: each value then within 2^-22 of itself and 2^-39 of its row's largest
+ * |dlogits| max|centroid|, a centroid within 2^-39 of its largest element.  A
+ * dlogits beyond bf16's range makes NaN of the results that it enters.  No
+ * buffer written may overlap one read, but for du on du_base.
+ * An index outside [0, E) records MOE_DEVERR_BAD_INDEX and its gate part is
+ * left out.  T == 0 sets dcentroids to zero.
  * Limits: as moe_route (d % 128 == 0, E % 16 == 0, 16 <= E <= 1024, K <= E,
  * K <= 32), ldu % 8 == 0, T % seq_len == 0.
  */
