@@ -290,7 +290,8 @@ class MoELayer:
         upstream gradient of the balance loss of a layer built with
         balance_loss, None where the loss is not trained.
         A forward in between overwrites the routing: with router_grad that is
-        refused (replays of a captured forward do the same, unseen here).
+        refused.  Replays of captured calls are not seen here: capture
+        forward_train and backward together.
         Dgrad: dy (1x128 FP8) . W2 -> dh; SwiGLU backward on the cached FP8
         gu -> dgu (1x128 FP8); dgu . W1 -> dx; un-permute.  Wgrad: the
         token-major 128x1 operands dy^T, h^T (recomputed), dgu^T, x^T through

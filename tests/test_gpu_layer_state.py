@@ -53,3 +53,20 @@ def test_a_layer_without_router_gradient_is_not_asked(cuda_dev):
     got = layer.backward(dout)
     for k in ("du", "dW1", "dW2"):
         assert torch.equal(want[k], got[k]), k
+
+
+def test_a_training_step_captured_whole(cuda_dev):
+    """forward_train and backward in one graph, replayed after other passes."""
+    cfg, layer, u, dout = _layer(cuda_dev, router_grad=True)
+    layer.forward_train(u, update_bias=False)
+    want = {k: v.clone() for k, v in layer.backward(dout).items() if k in ("du", "dgate", "dlogits", "dcentroids")}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward_train(u, update_bias=False)
+        got = layer.backward(dout)
+    layer.forward(u.flip(0).contiguous(), update_bias=False)
+    graph.replay()
+    for k, v in want.items():
+        assert torch.equal(v, got[k]), k
+    del graph
